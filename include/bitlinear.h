@@ -24,7 +24,8 @@
  *     check returns its status and launches nothing.  A launch failure returns
  *     BL_ERR_CUDA.  A kernel that stops waiting on an internal barrier after its
  *     time limit records BL_ERR_TIMEOUT in a device status word, read back with
- *     bitlinear_device_status().
+ *     bitlinear_device_status(); a page table entry that is no page of the cache
+ *     is skipped and recorded there as BL_ERR_PAGE.
  *   - Shapes: M >= 0 tokens (M == 0 is a no-op returning BL_OK), K > 0 input
  *     features with K % 16 == 0 and K <= BL_MAX_K, N > 0 output features with
  *     N % 4 == 0.  Tensor pointers must be 16-byte aligned.
@@ -57,7 +58,8 @@ typedef enum {
     BL_ERR_WORKSPACE = 5, /* workspace missing or smaller than required */
     BL_ERR_CUDA = 6,      /* a CUDA launch or runtime call failed */
     BL_ERR_TIMEOUT = 7,   /* a device-side bounded wait expired */
-    BL_ERR_DEVICE = 8     /* no usable sm_100 device is current */
+    BL_ERR_DEVICE = 8,    /* no usable sm_100 device is current */
+    BL_ERR_PAGE = 9       /* a page table named a page outside the cache (device status) */
 } bl_status;
 
 typedef enum { BL_OUT_BF16 = 0, BL_OUT_F32 = 1 } bl_out_dtype;
@@ -454,11 +456,114 @@ bl_status bitlinear_attn_decode(const uint16_t* q, const uint16_t* k_cache, cons
                                 float scale, uint16_t* out, void* workspace, size_t workspace_bytes,
                                 void* stream);
 
+/* ---- paged key/value cache, and attention over it -------------------------- */
+
+typedef enum { BL_KV_BF16 = 0, BL_KV_I8 = 1 } bl_kv_format;
+
+/* A paged key/value cache (all pointers device, owned by the caller).  Element
+ * (page, slot, head, i) of k and of v lies at page * stride_page + slot *
+ * stride_slot + head * stride_head + i: [num_pages, page_size, kv_heads,
+ * head_dim] contiguous, a view of a larger tensor, or heads before slots.
+ * int8 rows (one position of one key/value head) carry a binary32 step each:
+ * a code stands for RN32(code * step).
+ *   head_dim 64 or 128; page_size a multiple of 16; k, v 16-byte aligned and
+ *   every stride a positive multiple of 16 bytes. */
+typedef struct {
+    void* k;               /* bf16 or int8 per format */
+    void* v;
+    float* k_step;         /* fp32 [num_pages, kv_heads, page_size], BL_KV_I8 only (else NULL) */
+    float* v_step;
+    int64_t num_pages;
+    int64_t page_size;
+    int64_t kv_heads;
+    int64_t head_dim;
+    int64_t stride_page;   /* in elements, the same for k and v */
+    int64_t stride_slot;
+    int64_t stride_head;
+    bl_kv_format format;
+} bl_kv_cache;
+
+/* The sequences of one step (device int32 arrays, read when the kernels run,
+ * so a captured graph replays with the arrays' contents of that moment).
+ * Sequence b has the rows cu_q[b] .. cu_q[b + 1] - 1 of the step's row buffers
+ * (its new tokens) and kv_len[b] positions in the cache, those of its new rows
+ * included: row i of its n rows stands at position kv_len[b] - n + i, and
+ * position p lies in page pages[b * max_pages + p / page_size], slot
+ * p % page_size.  Sequences may have no rows or no positions.  Rows behind
+ * cu_q[batch] (a padded batch) belong to no sequence: nothing of them is read
+ * or written.  Entries of the table past a sequence's positions are not used.
+ * Whatever the arrays hold, no access leaves the buffers: starts are cut to
+ * the row buffers, lengths to max_pages * page_size, and a needed entry that
+ * is no page of the cache records BL_ERR_PAGE in the device status (the
+ * results of that sequence are then unspecified). */
+typedef struct {
+    const int32_t* cu_q;   /* [batch + 1], ascending */
+    const int32_t* kv_len; /* [batch] */
+    const int32_t* pages;  /* [batch, max_pages] */
+    int64_t batch;
+    int64_t max_pages;
+} bl_kv_batch;
+
+/* Writes the new rows' keys and values into the cache.  BL_KV_BF16: as they
+ * are.  BL_KV_I8: the codes of bitlinear_act_quant per (row, key/value head),
+ *   s = RN32(127 / max(max|x|, 1e-5)), code = clamp(rint(RN32(x * s)), -128, 127),
+ *   step = RN32(1 / s);
+ * a row that holds an infinity or NaN is written as zero codes with a NaN
+ * step, so it reads as NaN.  Rows whose position is negative (more rows than
+ * positions) are not written.  Two rows of one call that the table puts in the
+ * same slot leave it unspecified which of them (or a mixture) is kept.
+ *   k, v       device bf16 [T, kv_heads, head_dim]; rows k_stride / v_stride
+ *              elements apart (slices of a fused projection), heads contiguous;
+ *              16-byte aligned, strides multiples of 8.
+ * T >= 0 rows; no workspace. */
+bl_status bitlinear_kv_write(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t T,
+                             void* stream);
+
+/* The inverse of bitlinear_kv_write: the rows of the batch read back out of
+ * the cache, RN_bf16(RN32(code * step)) for BL_KV_I8 (with cu_q counting every
+ * position of a sequence, the whole of it).  Rows that belong to no sequence,
+ * or whose position is negative, are left as they were.  k, v, strides and T
+ * as for bitlinear_kv_write, as outputs. */
+bl_status bitlinear_kv_read(const bl_kv_cache* cache, const bl_kv_batch* batch, uint16_t* k,
+                            int64_t k_stride, uint16_t* v, int64_t v_stride, int64_t T, void* stream);
+
+/* Workspace bitlinear_attn_paged needs for T rows (depends on the current
+ * device's SM count, not on the sequences' lengths). */
+bl_status bitlinear_attn_paged_workspace_size(int64_t T, int64_t q_heads, int64_t kv_heads,
+                                              int64_t head_dim, size_t* bytes);
+
+/* Grouped-query attention of the batch's new rows over the paged cache (which
+ * already holds their own keys and values): decode steps, drafted tokens,
+ * chunks of prompts and whole prompts, mixed in one batch.  As
+ * bitlinear_attn_decode,
+ *   out[r, h] = sum_j p_j v[j, g],  p = softmax_j((q[r, h] . k[j, g]) * scale),
+ * g = h / (q_heads / kv_heads), over the positions j of r's sequence: every
+ * one (causal 0), or those up to r's own position kv_len - n + i (causal 1).
+ * What a hidden position holds has no part in a result, infinities and NaN
+ * included.  A row that sees no position gets zeros.
+ * Scores, softmax and sums are binary32; the probabilities are rounded to bf16
+ * for the product with the values (relative 2^-8 each), the output to bf16.
+ *   q, out     device bf16 [T, q_heads, head_dim]; rows q_stride / out_stride
+ *              elements apart, heads contiguous; 16-byte aligned, strides
+ *              multiples of 8.  Rows of no sequence are left as they were.
+ *   scale      score multiplier, positive and finite (1/sqrt(head_dim) in the model).
+ *   workspace  device, 16-byte aligned, at least
+ *              bitlinear_attn_paged_workspace_size bytes.  A workspace serves
+ *              one call at a time; its contents need no initialisation and
+ *              nothing in it is kept for the next call.
+ * q_heads / kv_heads in 1 .. 128, T * q_heads <= INT32_MAX. */
+bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* q,
+                               int64_t q_stride, int64_t T, int64_t q_heads, float scale, int causal,
+                               uint16_t* out, int64_t out_stride, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* ---- device status -------------------------------------------------------- */
 
 /* Synchronises `stream`, then returns and clears the library's device status
- * word on the current device: BL_OK, or BL_ERR_TIMEOUT if a kernel gave up on a
- * bounded wait since the last call. */
+ * word on the current device: BL_OK, BL_ERR_TIMEOUT if a kernel gave up on a
+ * bounded wait since the last call, or (without a timeout) BL_ERR_PAGE if one
+ * met a page table entry that is no page of its cache. */
 bl_status bitlinear_device_status(void* stream);
 
 /* Failure-detection self-test (diagnostics; the pages have no counterpart).

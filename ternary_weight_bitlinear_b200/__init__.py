@@ -19,4 +19,6 @@ from .bitlinear import (BL_MAX_K, BL_OUT_BF16, BL_OUT_F32, BitLinearError, LIB_P
                         bitlinear_quantized_batch_workspace_size,
                         bitlinear_selftest_wait_timeout,
                         bitlinear_relu2_mul, bitlinear_unpack, lib, status_string,
-                        bitlinear_rope, bitlinear_attn_decode, bitlinear_attn_decode_workspace_size)
+                        bitlinear_rope, bitlinear_attn_decode, bitlinear_attn_decode_workspace_size,
+                        BL_KV_BF16, BL_KV_I8, make_kv_cache, make_kv_batch, bitlinear_kv_write,
+                        bitlinear_kv_read, bitlinear_attn_paged, bitlinear_attn_paged_workspace_size)

@@ -26,6 +26,8 @@
 #include "ste.cuh"
 #include "chain.cuh"
 #include "attn.cuh"
+#include "kvcache.cuh"
+#include "attn_paged.cuh"
 
 namespace {
 
@@ -579,6 +581,7 @@ const char* bitlinear_status_string(bl_status s) {
         case BL_ERR_CUDA: return "CUDA launch or runtime error";
         case BL_ERR_TIMEOUT: return "a device-side bounded wait expired";
         case BL_ERR_DEVICE: return "no usable sm_100 CUDA device is current";
+        case BL_ERR_PAGE: return "a page table names a page outside the cache";
     }
     return "unknown status";
 }
@@ -787,6 +790,73 @@ bl_status attn_launch_d(const AttnArgs& a, int group, int64_t splits, int64_t q_
     if (st != BL_OK) return st;
     return launch(attn_combine_kernel<D>, dim3((unsigned)q_heads), dim3(D), 0, stream,
                   (const float*)a.part, (int)splits, (int)q_heads, out);
+}
+
+// ---- paged key/value cache ---------------------------------------------------
+// Checks of what every entry point over the paged cache takes; fills the
+// kernels' view of the cache and of the batch.
+bl_status kv_check(const bl_kv_cache* c, const bl_kv_batch* b, int64_t T, KvCacheArgs* ca, KvBatchArgs* ba) {
+    if (!c || !b) return BL_ERR_NULL;
+    if (c->format != BL_KV_BF16 && c->format != BL_KV_I8) return BL_ERR_DTYPE;
+    const bool i8 = c->format == BL_KV_I8;
+    if (c->head_dim != 64 && c->head_dim != 128) return BL_ERR_SHAPE;
+    if (c->num_pages <= 0 || c->num_pages > INT32_MAX || c->page_size <= 0 || c->page_size % 16 != 0 ||
+        c->page_size > (1 << 20) || c->kv_heads <= 0 || c->kv_heads > 65535)
+        return BL_ERR_SHAPE;
+    if (b->batch < 0 || b->batch >= INT32_MAX || b->max_pages < 0 || b->max_pages > INT32_MAX) return BL_ERR_SHAPE;
+    if (T < 0 || T > INT32_MAX / c->kv_heads) return BL_ERR_SHAPE;
+    const int64_t unit = i8 ? 16 : 8, most = ((int64_t)1 << 40) / (i8 ? 1 : 2);
+    for (const int64_t s : {c->stride_page, c->stride_slot, c->stride_head}) {
+        if (s <= 0 || s >= most) return BL_ERR_SHAPE;
+        if (s % unit != 0) return BL_ERR_ALIGN;
+    }
+    if (!c->k || !c->v || (i8 && (!c->k_step || !c->v_step))) return BL_ERR_NULL;
+    if (!aligned16(c->k) || !aligned16(c->v) || (i8 && (!aligned16(c->k_step) || !aligned16(c->v_step))))
+        return BL_ERR_ALIGN;
+    if (T > 0 && b->batch > 0 && (!b->cu_q || !b->kv_len || (b->max_pages > 0 && !b->pages))) return BL_ERR_NULL;
+    ca->k = c->k;
+    ca->v = c->v;
+    ca->k_step = i8 ? c->k_step : nullptr;
+    ca->v_step = i8 ? c->v_step : nullptr;
+    ca->sp = c->stride_page;
+    ca->ss = c->stride_slot;
+    ca->sh = c->stride_head;
+    ca->num_pages = (int)c->num_pages;
+    ca->page_size = (int)c->page_size;
+    ca->kv_heads = (int)c->kv_heads;
+    ba->cu_q = b->cu_q;
+    ba->kv_len = b->kv_len;
+    ba->pages = b->pages;
+    ba->batch = (int)b->batch;
+    ba->max_pages = (int)b->max_pages;
+    ba->T = (int)T;
+    ba->max_len = (int)std::min<int64_t>(b->max_pages * c->page_size, INT32_MAX);
+    return BL_OK;
+}
+
+// A row buffer [T, heads, head_dim] with rows `stride` elements apart.
+bl_status kv_rows_check(const void* p, int64_t stride, int64_t width) {
+    if (stride < width || stride > INT64_MAX / INT32_MAX) return BL_ERR_SHAPE;
+    if (!p) return BL_ERR_NULL;
+    return aligned16(p) && stride % 8 == 0 ? BL_OK : BL_ERR_ALIGN;
+}
+
+unsigned kv_grid(int64_t T, int64_t kv_heads, int64_t head_dim) {
+    const int64_t groups = kKvThreads / (head_dim / 8);
+    return (unsigned)((T * kv_heads + groups - 1) / groups);
+}
+
+bl_status attn_paged_check(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
+    if (head_dim != 64 && head_dim != 128) return BL_ERR_SHAPE;
+    if (kv_heads <= 0 || kv_heads > 65535 || q_heads <= 0 || q_heads % kv_heads != 0 || q_heads / kv_heads > 128)
+        return BL_ERR_SHAPE;
+    return T < 0 || T > INT32_MAX / q_heads ? BL_ERR_SHAPE : BL_OK;
+}
+
+template <int D, bool I8>
+bl_status attn_paged_launch(const PagedAttnArgs& a, cudaStream_t stream) {
+    const int64_t warps = (int64_t)a.b.T * a.heads;
+    return launch(attn_paged_row_kernel<D, I8>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, a);
 }
 
 }  // namespace
@@ -1225,6 +1295,88 @@ bl_status bitlinear_attn_decode(const uint16_t* q, const uint16_t* k_cache, cons
                            : attn_launch_d<64>(a, group, splits, q_heads, out, s);
 }
 
+// ---- paged key/value cache, and attention over it ------------------------------
+
+bl_status bitlinear_kv_write(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* k,
+                             int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t T,
+                             void* stream) {
+    KvCacheArgs c;
+    KvBatchArgs b;
+    bl_status st;
+    if ((st = kv_check(cache, batch, T, &c, &b)) != BL_OK) return st;
+    if (T == 0 || batch->batch == 0) return BL_OK;
+    const int64_t width = cache->kv_heads * cache->head_dim;
+    if ((st = kv_rows_check(k, k_stride, width)) != BL_OK || (st = kv_rows_check(v, v_stride, width)) != BL_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != BL_OK) return st;
+    const bool i8 = cache->format == BL_KV_I8;
+    auto kernel = cache->head_dim == 128 ? (i8 ? kv_write_kernel<128, true> : kv_write_kernel<128, false>)
+                                         : (i8 ? kv_write_kernel<64, true> : kv_write_kernel<64, false>);
+    return launch(kernel, dim3(kv_grid(T, cache->kv_heads, cache->head_dim)), dim3(kKvThreads), 0,
+                  static_cast<cudaStream_t>(stream), c, b, k, k_stride, v, v_stride);
+}
+
+bl_status bitlinear_kv_read(const bl_kv_cache* cache, const bl_kv_batch* batch, uint16_t* k,
+                            int64_t k_stride, uint16_t* v, int64_t v_stride, int64_t T, void* stream) {
+    KvCacheArgs c;
+    KvBatchArgs b;
+    bl_status st;
+    if ((st = kv_check(cache, batch, T, &c, &b)) != BL_OK) return st;
+    if (T == 0 || batch->batch == 0) return BL_OK;
+    const int64_t width = cache->kv_heads * cache->head_dim;
+    if ((st = kv_rows_check(k, k_stride, width)) != BL_OK || (st = kv_rows_check(v, v_stride, width)) != BL_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != BL_OK) return st;
+    const bool i8 = cache->format == BL_KV_I8;
+    auto kernel = cache->head_dim == 128 ? (i8 ? kv_read_kernel<128, true> : kv_read_kernel<128, false>)
+                                         : (i8 ? kv_read_kernel<64, true> : kv_read_kernel<64, false>);
+    return launch(kernel, dim3(kv_grid(T, cache->kv_heads, cache->head_dim)), dim3(kKvThreads), 0,
+                  static_cast<cudaStream_t>(stream), c, b, k, k_stride, v, v_stride);
+}
+
+bl_status bitlinear_attn_paged_workspace_size(int64_t T, int64_t q_heads, int64_t kv_heads,
+                                              int64_t head_dim, size_t* bytes) {
+    if (!bytes) return BL_ERR_NULL;
+    bl_status st;
+    if ((st = attn_paged_check(T, q_heads, kv_heads, head_dim)) != BL_OK) return st;
+    *bytes = 0;
+    return BL_OK;
+}
+
+bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* q,
+                               int64_t q_stride, int64_t T, int64_t q_heads, float scale, int causal,
+                               uint16_t* out, int64_t out_stride, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    PagedAttnArgs a = {};
+    bl_status st;
+    if ((st = kv_check(cache, batch, T, &a.c, &a.b)) != BL_OK) return st;
+    if ((st = attn_paged_check(T, q_heads, cache->kv_heads, cache->head_dim)) != BL_OK) return st;
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return BL_ERR_SHAPE;
+    if (T == 0 || batch->batch == 0) return BL_OK;
+    const int64_t width = q_heads * cache->head_dim;
+    if ((st = kv_rows_check(q, q_stride, width)) != BL_OK || (st = kv_rows_check(out, out_stride, width)) != BL_OK)
+        return st;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != BL_OK) return st;
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.o_stride = out_stride;
+    a.heads = (int)q_heads;
+    a.group = (int)(q_heads / cache->kv_heads);
+    a.causal = causal != 0;
+    a.qscale = scale * kLog2e;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cache->format == BL_KV_I8)
+        return cache->head_dim == 128 ? attn_paged_launch<128, true>(a, s) : attn_paged_launch<64, true>(a, s);
+    return cache->head_dim == 128 ? attn_paged_launch<128, false>(a, s) : attn_paged_launch<64, false>(a, s);
+}
+
 bl_status bitlinear_device_status(void* stream) {
     int dev;
     DeviceInfo info;
@@ -1242,7 +1394,7 @@ bl_status bitlinear_device_status(void* stream) {
         cudaGetLastError();
         return BL_ERR_CUDA;
     }
-    return (v & kStatusTimeout) ? BL_ERR_TIMEOUT : BL_OK;
+    return (v & kStatusTimeout) ? BL_ERR_TIMEOUT : (v & kStatusBadPage) ? BL_ERR_PAGE : BL_OK;
 }
 
 bl_status bitlinear_selftest_wait_timeout(int64_t limit_ns, void* stream) {

@@ -13,10 +13,12 @@ namespace bl {
 
 constexpr float kScaleFloor = 1e-5f;  // clamp floor of both scales (absmean, absmax)
 
-// Device status word: bit 0 = a bounded wait expired.  Read and cleared by
+// Device status word: bit 0 = a bounded wait expired, bit 1 = a page table
+// named a page that the cache does not have.  Read and cleared by
 // bitlinear_device_status().
 __device__ unsigned int g_status;
 constexpr unsigned int kStatusTimeout = 1u;
+constexpr unsigned int kStatusBadPage = 2u;
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t b) {

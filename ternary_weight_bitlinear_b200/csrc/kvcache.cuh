@@ -1,0 +1,211 @@
+// kvcache.cuh -- the paged key/value cache: new rows written into it
+// (quantised per row when the cache holds int8) and read back out of it.
+//
+// A batch is described by three device arrays: cu_q[b] is the first new row
+// of sequence b, kv_len[b] its positions (the new ones included), and
+// pages[b, p / page_size] the page that holds position p.  Row i of the n
+// new rows of a sequence stands at position kv_len - n + i, so the write, the
+// read and the attention share one description of a step.
+//
+// int8 rows: the activation quantiser's codes (quant.cuh) per (position,
+// key/value head), s = RN32(127 / max(max|x|, 1e-5)),
+// code = clamp(rint(RN32(x s)), -128, 127), and step = RN32(1 / s) kept in
+// binary32 beside them; a code stands for RN32(code step).  A row that holds
+// an infinity or NaN has no scale: it is written as zero codes with a NaN
+// step, so every reader of that row (and no other) gets NaN.
+//
+// Both kernels move each row once and are bound by HBM bytes (for a few rows
+// by latency: the row's sequence, its length and its page are three dependent
+// loads).  A group of d/8 lanes takes one (row, head): 16 bytes a lane, both
+// the key and the value in flight before the lookups begin; the row's
+// maximum costs log2(d/8) shuffles.
+#pragma once
+
+#include "common.cuh"
+
+namespace bl {
+
+constexpr int kKvThreads = 128;
+
+struct KvCacheArgs {
+    void* k;                     // bf16 or int8 pages
+    void* v;
+    float* k_step;               // [num_pages, kv_heads, page_size] (int8 only)
+    float* v_step;
+    int64_t sp, ss, sh;          // strides in elements: page, slot, head
+    int num_pages, page_size, kv_heads;
+};
+
+struct KvBatchArgs {
+    const int32_t* cu_q;         // [batch + 1]
+    const int32_t* kv_len;       // [batch]
+    const int32_t* pages;        // [batch, max_pages]
+    int batch;
+    int max_pages;
+    int T;                       // rows the caller's buffers have
+    int max_len;                 // max_pages * page_size, at most INT32_MAX
+};
+
+// A sequence as the kernels see it: whatever the arrays hold, the rows lie
+// inside [0, T) and the length inside the page table.
+struct KvSeq {
+    int q0, n, len;
+};
+
+__device__ __forceinline__ KvSeq kv_seq(const KvBatchArgs& a, int b) {
+    KvSeq s;
+    s.q0 = min(max(__ldcg(a.cu_q + b), 0), a.T);
+    s.n = max(min(__ldcg(a.cu_q + b + 1), a.T) - s.q0, 0);
+    s.len = min(max(__ldcg(a.kv_len + b), 0), a.max_len);
+    return s;
+}
+
+// The sequence of row t, searched by a whole warp: the number of starts
+// cu_q[1..batch] at or below t (batch when no sequence has the row).  The
+// starts are in ascending order, so empty sequences are passed over.
+__device__ __forceinline__ int kv_seq_of_row(const KvBatchArgs& a, int t, int lane) {
+    int count = 0;
+    for (int i = 0; i < a.batch; i += 32) {
+        const bool below = i + lane < a.batch && __ldcg(a.cu_q + 1 + i + lane) <= t;
+        const uint32_t m = __ballot_sync(0xffffffffu, below);
+        count += __popc(m);
+        if (m != 0xffffffffu) break;
+    }
+    return count;
+}
+
+// Page of position p of sequence b, or -1 (recorded in the status word) when
+// the table's entry is not a page of the cache.
+__device__ __forceinline__ int kv_page(const KvCacheArgs& c, const KvBatchArgs& a, int b, int p) {
+    const int page = __ldcg(a.pages + (int64_t)b * a.max_pages + p / c.page_size);
+    if ((unsigned)page < (unsigned)c.num_pages) return page;
+    atomicOr(&g_status, kStatusBadPage);
+    return -1;
+}
+
+// Where this group's row lies in the cache: element offset of (page, slot,
+// head) and of its step; false when the row has no place.
+__device__ __forceinline__ bool kv_place(const KvCacheArgs& c, const KvBatchArgs& a, int t, int head,
+                                         int b, int64_t* off, int64_t* step_off) {
+    while (b < a.batch && __ldcg(a.cu_q + b + 1) <= t) ++b;  // this group's row may be a later one than the warp's first
+    if (b >= a.batch) return false;
+    const KvSeq s = kv_seq(a, b);
+    const int pos = s.len - s.n + (t - s.q0);
+    if (t < s.q0 || pos < 0) return false;
+    const int page = kv_page(c, a, b, pos);
+    if (page < 0) return false;
+    const int slot = pos % c.page_size;
+    *off = page * c.sp + slot * c.ss + head * c.sh;
+    *step_off = ((int64_t)page * c.kv_heads + head) * c.page_size + slot;
+    return true;
+}
+
+// Largest |x| of eight bf16 values, as bf16 bits (above every finite value
+// when one is an infinity or NaN).
+__device__ __forceinline__ uint32_t kv_absmax8(const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    return max(m & 0xFFFFu, m >> 16);
+}
+
+// Eight codes of one row's scale.
+__device__ __forceinline__ uint2 kv_codes8(const uint4& x, float s) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t r[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = bf16_bits_to_float((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+        const int c = min(max(__float2int_rn(__fmul_rn(f, s)), -128), 127);
+        r[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
+    }
+    return make_uint2(r[0], r[1]);
+}
+
+// One row quantised by its group of LANES lanes.
+template <int LANES>
+__device__ __forceinline__ void kv_store_i8(const uint4& x, int8_t* dst, float* step, int part, bool live) {
+    uint32_t m = kv_absmax8(x);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!live) return;
+    const bool finite = m < 0x7F80u;
+    const float s = __fdiv_rn(127.0f, fmaxf(bf16_bits_to_float(m), kScaleFloor));
+    *reinterpret_cast<uint2*>(dst + part * 8) = finite ? kv_codes8(x, s) : make_uint2(0, 0);
+    if (part == 0) *step = finite ? __frcp_rn(s) : __int_as_float(0x7FC00000);
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCacheArgs c, const KvBatchArgs a,
+                                                              const uint16_t* __restrict__ k, int64_t k_stride,
+                                                              const uint16_t* __restrict__ v, int64_t v_stride) {
+    constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
+    const int lane = threadIdx.x & 31, part = threadIdx.x % LANES;
+    const int64_t pairs = (int64_t)a.T * c.kv_heads;
+    const int64_t warp_pair = (int64_t)blockIdx.x * GROUPS + (threadIdx.x & ~31) / LANES;
+    const int64_t pair = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp_pair >= pairs) return;  // warp-uniform
+    const bool have = pair < pairs;
+    const int t = (int)((have ? pair : warp_pair) / c.kv_heads), head = (int)((have ? pair : warp_pair) % c.kv_heads);
+    const uint4 kx = __ldcg(reinterpret_cast<const uint4*>(k + t * k_stride + head * D) + part);
+    const uint4 vx = __ldcg(reinterpret_cast<const uint4*>(v + t * v_stride + head * D) + part);
+    const int b = kv_seq_of_row(a, (int)(warp_pair / c.kv_heads), lane);
+    int64_t off = 0, step_off = 0;
+    const bool live = have && kv_place(c, a, t, head, b, &off, &step_off);
+    if constexpr (I8) {
+        kv_store_i8<LANES>(kx, static_cast<int8_t*>(c.k) + off, c.k_step + step_off, part, live);
+        kv_store_i8<LANES>(vx, static_cast<int8_t*>(c.v) + off, c.v_step + step_off, part, live);
+    } else if (live) {
+        *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.k) + off) + part) = kx;
+        *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.v) + off) + part) = vx;
+    }
+}
+
+// Eight bf16 values of eight codes: RN_bf16(RN32(code * step)).
+__device__ __forceinline__ uint4 kv_values8(const uint2& c, float step) {
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
+        const float lo = __fmul_rn((float)(int8_t)(w & 0xFF), step);
+        const float hi = __fmul_rn((float)(int8_t)((w >> 8) & 0xFF), step);
+        r[i] = pack_bf16x2(lo, hi);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCacheArgs c, const KvBatchArgs a,
+                                                             uint16_t* __restrict__ k, int64_t k_stride,
+                                                             uint16_t* __restrict__ v, int64_t v_stride) {
+    constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
+    const int lane = threadIdx.x & 31, part = threadIdx.x % LANES;
+    const int64_t pairs = (int64_t)a.T * c.kv_heads;
+    const int64_t warp_pair = (int64_t)blockIdx.x * GROUPS + (threadIdx.x & ~31) / LANES;
+    const int64_t pair = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp_pair >= pairs) return;
+    const int b = kv_seq_of_row(a, (int)(warp_pair / c.kv_heads), lane);
+    if (pair >= pairs) return;
+    const int t = (int)(pair / c.kv_heads), head = (int)(pair % c.kv_heads);
+    int64_t off, step_off;
+    if (!kv_place(c, a, t, head, b, &off, &step_off)) return;
+    uint4 kx, vx;
+    if constexpr (I8) {
+        const uint2 kc = __ldcg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(c.k) + off) + part);
+        const uint2 vc = __ldcg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(c.v) + off) + part);
+        kx = kv_values8(kc, __ldcg(c.k_step + step_off));
+        vx = kv_values8(vc, __ldcg(c.v_step + step_off));
+    } else {
+        kx = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.k) + off) + part);
+        vx = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.v) + off) + part);
+    }
+    *(reinterpret_cast<uint4*>(k + t * k_stride + head * D) + part) = kx;
+    *(reinterpret_cast<uint4*>(v + t * v_stride + head * D) + part) = vx;
+}
+
+}  // namespace bl

@@ -495,7 +495,8 @@ typedef struct {
  * Whatever the arrays hold, no access leaves the buffers: starts are cut to
  * the row buffers, lengths to max_pages * page_size, and a needed entry that
  * is no page of the cache records BL_ERR_PAGE in the device status (the
- * results of that sequence are then unspecified). */
+ * results of that sequence are then unspecified).
+ *   max_pages * page_size <= 2^30. */
 typedef struct {
     const int32_t* cu_q;   /* [batch + 1], ascending */
     const int32_t* kv_len; /* [batch] */

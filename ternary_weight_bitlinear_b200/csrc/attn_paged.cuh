@@ -4,15 +4,52 @@
 //   out[r, h] = sum_j p_j v_j,  p = softmax_j(scale q[r, h] . k_j),
 // j over the positions of r's sequence (up to r's own when causal), key/value
 // head h / (H / H_kv).  A row that sees no position gets zeros.
+//
+// One kernel for every mixture of decode rows, drafted tokens, chunks and
+// prompts, on the tensor cores:
+//  * Tiles.  A sub-tile is 128 rows of one sequence and key/value head: 128 /
+//    group tokens times the group's heads, so keys and values are read once
+//    for the group.  Per tile of 128 positions S = Q K^T and O += P V are
+//    tcgen05.mma (M = 128) with S, P (bf16, over S's columns) and O in tensor
+//    memory; a softmax thread owns a row: no shuffles.
+//  * Work.  An item is two sub-tiles (or a sequence's last, single one) of one
+//    key/value head.  The items' tiles are laid end to end over sequences,
+//    heads and sub-tiles, and every CTA (one per SM) takes an equal share of
+//    them, found from the lengths on the device: no length is known on the
+//    host, a captured call replays with other lengths, and one long sequence
+//    spreads over the GPU as well as many short ones.  An item cut by shares
+//    leaves (max, sum, vector) partials, merged by attn_merge_kernel in the
+//    order of the CTAs: results do not depend on timing.
+//  * Two softmax warpgroups.  In a pair item each has one sub-tile; in a
+//    single item they take alternate position tiles of the same rows and
+//    merge at the end.  While one works on its scores the tensor core runs the
+//    other's products: PV of a tile, then QK of the same group's next one.
+//  * Loads.  Pages arrive by TMA (a box per page part, no multicast) into a
+//    ring that holds K and V tiles in turn, running ahead across items.  int8
+//    pages land in a raw ring; a converter warpgroup writes their codes, exact
+//    in bf16, in the operand layout; the steps multiply scores (K) and
+//    probabilities (V) in binary32.
+//  * Rows behind an item's last position are no part of the values' product:
+//    its K extent ends at the last 16 positions, where the rows left are zeroed.
+// The running maximum moves only when a tile's exceeds it by 2^8 (the sums
+// stay far inside binary32), so O is seldom rescaled.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include "attn.cuh"
 #include "common.cuh"
+#include "gemm_tc.cuh"
 #include "kvcache.cuh"
+#include "skinny.cuh"
 
 namespace bl {
+
+constexpr int kPaRows = 128;     // rows of a sub-tile (MMA M)
+constexpr int kPaTile = 128;     // positions of a tile
+constexpr int kPaItemUnits = 1;  // cost of an item beside its tiles, in tiles of one sub-tile
+constexpr float kPaMaxGrowth = 8.0f;  // log2 growth of the maximum that a row's sums absorb
 
 struct PagedAttnArgs {
     KvCacheArgs c;
@@ -22,61 +59,1113 @@ struct PagedAttnArgs {
     int64_t q_stride, o_stride;
     int heads;
     int group;           // heads / kv_heads
+    int tokens;          // tokens of a sub-tile: 128 / group
     int causal;
+    int box;             // positions of a page box: the largest power of two up to 128 dividing page_size
     float qscale;        // scale * log2(e)
+    // workspace
+    float* part;         // [grid, 2, part_rows, D] unnormalised vectors
+    float* part_ml;      // [grid, 2, part_rows, 2] maximum (log2 domain) and sum
+    int4* desc;          // [grid, 2] what the CTA left (PaDesc)
+    int part_rows;
 };
 
-// One warp per (row, head); a lane holds D/32 dimensions of the query and of
-// the running output, and every position costs one dot product over the warp.
+// What a CTA left in the workspace.  Word 0 of desc[2 c]: the state of its
+// first share -- 0 nothing, 1 a continuing part of an item, 2 the end of one;
+// desc[2 c + 1]: an item that begins in this CTA and does not end there
+// (x: tokens, 0 for none; y: first row; z: key/value head; w: positions that
+// its first token sees, below zero where it has no place).
+
+// ---- items ------------------------------------------------------------------
+// An item and this CTA's part of it, as the scheduler warp leaves it in shared
+// memory for the other roles.
+struct PaItem {
+    int b, g;        // sequence, key/value head; b < 0: no more items
+    int row;         // first token's row in the batch
+    int tokens;      // tokens of the item
+    int nsub;        // sub-tiles: 1 or 2
+    int nt;          // position tiles of the item
+    int t0, t1;      // those of this CTA
+    int nt0;         // tiles up to t1 that the first sub-tile sees
+    int end;         // positions that some row of the item sees
+    int vend;        // positions that its first token sees; below zero where it has no place
+    int len;         // positions of the sequence
+    int pad[4];
+};
+constexpr int kPaItems = 4;      // ring of items
+
+__device__ __forceinline__ int pa_tiles(int end) { return (end + kPaTile - 1) / kPaTile; }
+
+// Positions that a row with `tok_end` tokens of its sequence up to and with itself sees.
+__device__ __forceinline__ int pa_end(const PagedAttnArgs& a, const KvSeq& s, int tok_end) {
+    return a.causal ? min(max(s.len - s.n + tok_end, 0), s.len) : s.len;
+}
+__device__ __forceinline__ int pa_items(const PagedAttnArgs& a, int n) {
+    const int subs = (n + a.tokens - 1) / a.tokens;
+    return (subs + 1) / 2;
+}
+// Cost of item i of a sequence, and its shape.
+__device__ __forceinline__ int pa_cost(const PagedAttnArgs& a, const KvSeq& s, int i, int* nsub, int* nt) {
+    const int first = 2 * i * a.tokens;
+    *nsub = s.n > first + a.tokens ? 2 : 1;
+    *nt = pa_tiles(pa_end(a, s, min(first + *nsub * a.tokens, s.n)));
+    return kPaItemUnits + *nsub * *nt;
+}
+
+// Walks the items of this CTA's share in unit order (the scheduler warp).
+struct PaWalk {
+    const PagedAttnArgs& a;
+    int64_t u0, u1;      // this CTA's units
+    int64_t at;          // first unit of the current item
+    int b, g, i;         // current item: sequence, head, index within (sequence, head)
+    KvSeq s;
+    int items;           // items per head of the sequence
+
+    __device__ __forceinline__ PaWalk(const PagedAttnArgs& args, const int64_t* plan) : a(args) {
+        u0 = plan[0];
+        u1 = plan[1];
+        at = plan[2];
+        b = (int)plan[3];
+        g = (int)plan[4];
+        i = (int)plan[5];
+        if (at < u1) load();
+    }
+    __device__ __forceinline__ void load() {
+        s = kv_seq(a.b, b);
+        items = pa_items(a, s.n);
+    }
+    __device__ __forceinline__ bool next(PaItem& it) {
+        while (at < u1) {
+            int nsub, nt;
+            const int c = pa_cost(a, s, i, &nsub, &nt);
+            const int64_t from = u0 - at, to = u1 - at;
+            const int lo = from > kPaItemUnits ? (int)((from - kPaItemUnits + nsub - 1) / nsub) : 0;
+            const int hi = to >= c ? nt : to > kPaItemUnits ? (int)((to - kPaItemUnits + nsub - 1) / nsub) : 0;
+            const int first = 2 * i * a.tokens;
+            it.b = b;
+            it.g = g;
+            it.row = s.q0 + first;
+            it.tokens = min(nsub * a.tokens, s.n - first);
+            it.nsub = nsub;
+            it.nt = nt;
+            it.t0 = lo;
+            it.t1 = hi;
+            it.nt0 = nsub == 2 ? min(hi, pa_tiles(pa_end(a, s, first + a.tokens))) : hi;
+            it.end = pa_end(a, s, first + it.tokens);
+            it.vend = a.causal ? s.len - s.n + first + 1 : s.len;
+            it.len = s.len;
+            const bool mine = lo < hi || (nt == 0 && from <= 0);
+            at += c;
+            if (++i == items) {
+                i = 0;
+                if (++g == a.c.kv_heads) {
+                    g = 0;
+                    while (++b < a.b.batch) {
+                        load();
+                        if (s.n > 0) break;
+                    }
+                    if (b >= a.b.batch) at = u1;  // past the last item
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+// Units of one head of sequence b.
+__device__ __forceinline__ int64_t pa_seq_units(const PagedAttnArgs& a, int b) {
+    const KvSeq s = kv_seq(a.b, b);
+    const int items = pa_items(a, s.n);
+    int64_t u = 0;
+    for (int i = 0; i < items; ++i) {
+        int nsub, nt;
+        u += pa_cost(a, s, i, &nsub, &nt);
+    }
+    return u;
+}
+
+// Inclusive scan over the CTA (blockDim.x threads, a multiple of 32).
+__device__ __forceinline__ int64_t pa_scan(int64_t v, int64_t* warp_sums, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+        if (w == warp) before = all;
+        all += warp_sums[w];
+    }
+    __syncthreads();
+    *total = all;
+    return v + before;
+}
+
+// This CTA's share of all units, and the item that its first unit lies in:
+// plan = {u0, u1, first unit of that item, sequence, head, item}.  Every
+// thread of the CTA calls it; warp_sums has 16 words.
+__device__ __forceinline__ void pa_plan(const PagedAttnArgs& a, int64_t* plan, int64_t* warp_sums) {
+    const int nthr = blockDim.x;
+    int64_t total = 0, mine = 0, upto = 0;
+    for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
+        const int b = b0 + threadIdx.x;
+        mine = b < a.b.batch ? pa_seq_units(a, b) * a.c.kv_heads : 0;
+        int64_t sum;
+        upto = total + pa_scan(mine, warp_sums, &sum);
+        total += sum;
+    }
+    const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    if (threadIdx.x == 0) {
+        plan[0] = u0;
+        plan[1] = u1;
+        plan[2] = u1;  // nothing, unless found below
+        plan[3] = plan[4] = plan[5] = 0;
+    }
+    __syncthreads();
+    if (u0 >= u1) return;
+    int64_t sum = 0;
+    for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
+        const int b = b0 + threadIdx.x;
+        if (a.b.batch > nthr) {  // several passes: scan again
+            mine = b < a.b.batch ? pa_seq_units(a, b) * a.c.kv_heads : 0;
+            int64_t s;
+            upto = sum + pa_scan(mine, warp_sums, &s);
+            sum += s;
+        }
+        if (mine > 0 && u0 >= upto - mine && u0 < upto) {
+            const int64_t per = mine / a.c.kv_heads, off = u0 - (upto - mine);
+            const int g = (int)(off / per);
+            int64_t at = upto - mine + g * per;
+            const KvSeq s = kv_seq(a.b, b);
+            int i = 0;
+            for (;;) {
+                int nsub, nt;
+                const int c = pa_cost(a, s, i, &nsub, &nt);
+                if (u0 < at + c) break;
+                at += c;
+                ++i;
+            }
+            plan[2] = at;
+            plan[3] = b;
+            plan[4] = g;
+            plan[5] = i;
+        }
+    }
+    __syncthreads();
+}
+
 template <int D, bool I8>
-__global__ void __launch_bounds__(128) attn_paged_row_kernel(const PagedAttnArgs a) {
+struct PaCfg {
+    static constexpr int kHalves = D / 64;                    // 64-column (128-byte) halves of a bf16 tile
+    static constexpr int kHalfBytes = kPaTile * 128;
+    static constexpr int kTileBytes = kHalves * kHalfBytes;   // a bf16 tile of K, V or Q
+    static constexpr int kStages = I8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 10);  // K and V operand ring
+    static constexpr int kRawBytes = kPaTile * D;             // an int8 tile
+    static constexpr int kRaw = I8 ? (D == 128 ? 3 : 8) : 0;
+    static constexpr int kSteps = I8 ? 4 : 0;                 // ring of the tiles' steps (K and V)
+    static constexpr int kThreads = I8 ? 512 : 384;
+    // registers a thread: the launch's (65536 / kThreads, in eights), and each role's share of the same total
+    static constexpr int kRegs = I8 ? 128 : 168, kRegsSoft = I8 ? 184 : 216, kRegsRest = 72, kRegsConv = 72;
+    static_assert(2 * kRegsSoft + kRegsRest + (I8 ? kRegsConv : 0) <= kRegs * (kThreads / 128), "register shares");
+    static constexpr int kOffRing = 2 * kTileBytes;           // after two Q slots
+    static constexpr int kOffRaw = kOffRing + kStages * kTileBytes;
+    static constexpr int kOffStep = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kOffMl = kOffStep + kSteps * 2 * kPaTile * 4;  // second group's (max, sum)
+    static constexpr int kOffItems = kOffMl + kPaRows * 8;
+    static constexpr int kOffOpen = kOffItems + kPaItems * (int)sizeof(PaItem);  // the MMA issuer's own
+    static constexpr int kOffBar = kOffOpen + kPaItems * (int)sizeof(PaItem);
+    // barriers: operand ring full/empty, raw full/empty, steps full/empty, Q full/empty,
+    // scores, probabilities, output done (one per group), merge full/empty, drain, items full/empty
+    static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kSteps + 4 + 6 + 2 + 1 + 2 * kPaItems;
+    static constexpr int kOffPlan = kOffBar + 8 * kBars;
+    static constexpr int kSmem = kOffPlan + 256 + 1024;       // plan words, alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+};
+
+// ---- tcgen05 and TMA wrappers -------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+// bf16 x bf16 -> binary32: A and B from shared memory.
+__device__ __forceinline__ void tc_mma_f16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// A from tensor memory.
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptors: binary32 accumulate, bf16 A and B, M = 128; N = 128
+// positions with B (keys) K-major, or N = D with B (values) N-major.
+constexpr uint32_t kPaIdescQk = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPaTile >> 3) << 17) |
+                                ((uint32_t)(kPaRows >> 4) << 24);
+template <int D>
+constexpr uint32_t pa_idesc_pv() {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D >> 3) << 17) |
+           ((uint32_t)(kPaRows >> 4) << 24);
+}
+// Values: rows are positions (the contraction), 128-byte-swizzled halves of 64
+// columns: 8-row groups 1024 bytes apart (stride offset), halves kHalfBytes
+// apart (leading offset).
+__device__ __forceinline__ uint64_t pa_desc_v(uint32_t addr, int half_bytes) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(half_bytes >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// 32 consecutive columns of this thread's lane (no wait).
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+        " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31},"
+        " [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Registers moved between the warpgroups of a CTA (every warp of a group calls it).
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Two binary32 operations at once.
+__device__ __forceinline__ void fma2(float& x, float& y, float bx, float by, float cx, float cy) {
+    asm("{\n\t.reg .b64 A, B, C;\n\t"
+        "mov.b64 A, {%0, %1};\n\tmov.b64 B, {%2, %3};\n\tmov.b64 C, {%4, %5};\n\t"
+        "fma.rn.f32x2 A, A, B, C;\n\tmov.b64 {%0, %1}, A;\n\t}"
+        : "+f"(x), "+f"(y) : "f"(bx), "f"(by), "f"(cx), "f"(cy));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float bx, float by) {
+    asm("{\n\t.reg .b64 A, B;\n\t"
+        "mov.b64 A, {%0, %1};\n\tmov.b64 B, {%2, %3};\n\t"
+        "mul.rn.f32x2 A, A, B;\n\tmov.b64 {%0, %1}, A;\n\t}"
+        : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
+    asm("{\n\t.reg .b64 A, B;\n\t"
+        "mov.b64 A, {%0, %1};\n\tmov.b64 B, {%2, %3};\n\t"
+        "add.rn.f32x2 A, A, B;\n\tmov.b64 {%0, %1}, A;\n\t}"
+        : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
+}
+
+// ---- the tasks of a CTA: (softmax group, position tile) in tensor-core order ----
+struct PaTask {
+    int w;             // softmax group
+    int t;             // position tile
+    int valid;         // positions of the tile that some row of the item sees
+    uint32_t tile;     // running number of the tile (its K and V ring places)
+    uint32_t slot;     // running number of the Q sub-tile
+    bool first, last;  // of this group in the item
+    bool frees;        // last task of the tile
+    bool ends;         // last task of the item
+    bool fresh;        // first task of the tile
+    int nsub;
+};
+
+struct PaTasks {
+    PaItem* open;         // items with tiles, kPaItems places: filled by the walk ahead, read by the one behind
+    uint32_t items, tile, slot;  // items opened, tiles and Q sub-tiles passed
+    int t, t0, t1, w, end, nt0, nsub;   // nsub 0: no item open
+    __device__ __forceinline__ explicit PaTasks(PaItem* o)
+        : open(o), items(0), tile(0), slot(0), t(0), t0(0), t1(0), w(0), end(0), nt0(0), nsub(0) {}
+    __device__ __forceinline__ void load() {
+        const PaItem& it = open[items++ % kPaItems];
+        t0 = t = it.t0;
+        t1 = it.t1;
+        nsub = it.nsub;
+        end = it.end;
+        nt0 = it.nt0;
+        w = nsub == 2 && t >= nt0 ? 1 : 0;
+    }
+    // The next task of the open item.
+    __device__ __forceinline__ void next(PaTask& k) {
+        k.t = t;
+        k.valid = min(kPaTile, end - t * kPaTile);
+        k.tile = tile;
+        k.nsub = nsub;
+        k.ends = false;
+        if (nsub == 2) {
+            k.w = w;
+            k.slot = slot + w;
+            k.first = t == t0;
+            k.last = t == (w == 0 ? nt0 : t1) - 1;
+            k.frees = w == 1;
+            k.fresh = w == 0 || t >= nt0;
+            if (w == 1) {
+                ++t;
+                ++tile;
+                w = t < nt0 ? 0 : 1;
+            } else {
+                w = 1;
+            }
+        } else {
+            k.w = (t - t0) & 1;
+            k.slot = slot;
+            k.first = t - t0 < 2;
+            k.last = t + 2 >= t1;
+            k.frees = k.fresh = true;
+            ++t;
+            ++tile;
+        }
+        if (t == t1) {
+            k.ends = true;
+            slot += nsub;
+            nsub = 0;
+        }
+    }
+};
+
+// ---- one row by a warp, position by position --------------------------------
+// The (max, sum, vector) of one row over positions [j0, j1) straight from the
+// cache, D/32 dimensions a lane, bf16 pages: only the positions that the row
+// sees take part, whatever the others hold.
+template <int D>
+__device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const uint16_t* qrow, int j0, int j1,
+                                    float (&o)[D / 32], float* m_out, float* l_out) {
     constexpr int DL = D / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    pdl_wait();
-    pdl_launch_dependents();
-    if (w >= (int64_t)a.b.T * a.heads) return;
-    const int t = (int)(w / a.heads), h = (int)(w % a.heads), g = h / a.group;
-    const int b = kv_seq_of_row(a.b, t, lane);
-    if (b >= a.b.batch) return;
-    const KvSeq s = kv_seq(a.b, b);
-    if (t < s.q0) return;
-    const int end = a.causal ? min(s.len, s.len - s.n + (t - s.q0) + 1) : s.len;
-    float q[DL], o[DL], m = -INFINITY, l = 0.0f;
+    float q[DL], m = -INFINITY, l = 0.0f;
 #pragma unroll
     for (int e = 0; e < DL; ++e) {
-        q[e] = bf16_bits_to_float(__ldcg(a.q + t * a.q_stride + h * D + lane * DL + e)) * a.qscale;
+        q[e] = bf16_bits_to_float(__ldcg(qrow + lane * DL + e)) * a.qscale;
         o[e] = 0.0f;
     }
-    for (int j = 0; j < end; ++j) {
+    for (int j = j0; j < j1; ++j) {
         const int page = kv_page(a.c, a.b, b, j), slot = j % a.c.page_size;
         if (page < 0) continue;
         const int64_t off = page * a.c.sp + slot * a.c.ss + g * a.c.sh + lane * DL;
-        const int64_t so = ((int64_t)page * a.c.kv_heads + g) * a.c.page_size + slot;
         float x = 0.0f, v[DL];
 #pragma unroll
         for (int e = 0; e < DL; ++e) {
-            float kk;
-            if constexpr (I8) {
-                kk = (float)__ldcg(static_cast<const int8_t*>(a.c.k) + off + e) * __ldcg(a.c.k_step + so);
-                v[e] = (float)__ldcg(static_cast<const int8_t*>(a.c.v) + off + e) * __ldcg(a.c.v_step + so);
-            } else {
-                kk = bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.k) + off + e));
-                v[e] = bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.v) + off + e));
-            }
-            x = fmaf(q[e], kk, x);
+            x = fmaf(q[e], bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.k) + off + e)), x);
+            v[e] = bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.v) + off + e));
         }
         x = warp_sum_f(x);
         const float mn = fmaxf(m, x);
-        const float alpha = mn == -INFINITY ? 1.0f : exp2f(m - mn), p = exp2f(x - mn);
+        const float alpha = m == mn ? 1.0f : exp2f(m - mn), p = mn == -INFINITY && x == x ? 0.0f : exp2f(x - mn);
         l = fmaf(l, alpha, p);
 #pragma unroll
-        for (int e = 0; e < DL; ++e) o[e] = fmaf(o[e], alpha, p * v[e]);
+        for (int e = 0; e < DL; ++e) o[e] = fmaf(p, v[e], o[e] * alpha);
         m = mn;
     }
+    *m_out = m;
+    *l_out = l;
+}
+
+// ---- the kernel -----------------------------------------------------------------
+template <int D, bool I8>
+__global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
+    const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PagedAttnArgs a) {
+    using C = PaCfg<D, I8>;
+    constexpr int NS = C::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = smem_raw + (base - raw);
+    const uint32_t bars = base + C::kOffBar;
+    auto full_bar = [&](int s) { return bars + 8u * s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (NS + s); };
+    auto rfull_bar = [&](int s) { return bars + 8u * (2 * NS + s); };
+    auto rempty_bar = [&](int s) { return bars + 8u * (2 * NS + C::kRaw + s); };
+    constexpr int kB1 = 2 * NS + 2 * C::kRaw;
+    auto sfull_bar = [&](int s) { return bars + 8u * (kB1 + s); };              // steps
+    auto sempty_bar = [&](int s) { return bars + 8u * (kB1 + C::kSteps + s); };
+    constexpr int kB2 = kB1 + 2 * C::kSteps;
+    auto qfull_bar = [&](int s) { return bars + 8u * (kB2 + s); };
+    auto qempty_bar = [&](int s) { return bars + 8u * (kB2 + 2 + s); };
+    auto score_bar = [&](int w) { return bars + 8u * (kB2 + 4 + w); };
+    auto prob_bar = [&](int w) { return bars + 8u * (kB2 + 6 + w); };
+    auto odone_bar = [&](int w) { return bars + 8u * (kB2 + 8 + w); };
+    const uint32_t mfull_bar = bars + 8u * (kB2 + 10), mempty_bar = bars + 8u * (kB2 + 11);
+    const uint32_t drain_bar = bars + 8u * (kB2 + 12);
+    const uint32_t item_bars = bars + 8u * (kB2 + 13);  // full, then empty
+    auto ifull_bar = [&](uint32_t i) { return item_bars + 8u * (i % kPaItems); };
+    auto iempty_bar = [&](uint32_t i) { return item_bars + 8u * (kPaItems + i % kPaItems); };
+    static_assert(kB2 + 13 + 2 * kPaItems == C::kBars, "barrier count");
+    PaItem* ring = reinterpret_cast<PaItem*>(sm + C::kOffItems);
+    int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // 6 words
+    int64_t* warp_sums = plan + 8;                                      // 16 words
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan + 24);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(full_bar(s), I8 ? 4 : 1);  // converter warps, or the loader's expect
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int s = 0; s < C::kRaw; ++s) {
+            mbar_init(rfull_bar(s), 1);
+            mbar_init(rempty_bar(s), 4);
+        }
+        for (int s = 0; s < C::kSteps; ++s) {
+            mbar_init(sfull_bar(s), 1);
+            mbar_init(sempty_bar(s), 8);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(qfull_bar(s), 1);
+            mbar_init(qempty_bar(s), 1);
+            mbar_init(score_bar(s), 1);
+            mbar_init(prob_bar(s), 4);
+            mbar_init(odone_bar(s), 1);
+        }
+        mbar_init(mfull_bar, 4);
+        mbar_init(mempty_bar, 4);
+        mbar_init(drain_bar, 1);
+        for (int i = 0; i < kPaItems; ++i) {
+            mbar_init(ifull_bar(i), 1);
+            mbar_init(iempty_bar(i), I8 ? 15 : 11);  // loaders, MMA issuer, softmax (and converter) warps
+        }
+        mbar_init_fence();
+    }
+    if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // columns: scores (and probabilities) of group w at 128 w, output of group w at 256 + 128 w
+    pdl_wait();
+    pdl_launch_dependents();
+    pa_plan(a, plan, warp_sums);
+
+    bool ok = true;
+    uint32_t ii = 0;  // items taken from the ring
+    // the next item for a whole warp (nullptr: none left, or a wait ran out), and its release
+    auto take = [&]() -> const PaItem* {
+        ok = __all_sync(0xffffffffu, mbar_wait(ifull_bar(ii), (ii / kPaItems) & 1u));
+        if (!ok) return nullptr;
+        const PaItem* it = ring + ii % kPaItems;
+        return it->b < 0 ? nullptr : it;
+    };
+    auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty_bar(ii));
+        ++ii;
+    };
+    if (warp < 4) {
+    setmaxnreg_dec<C::kRegsRest>();
+    if (warp == 3) {
+        // ---------------- scheduler ----------------
+        if (lane == 0) {
+            PaWalk walk(a, plan);
+            PaItem it;
+            for (bool more = true; more && ok; ++ii) {
+                more = walk.next(it);
+                if (!more) it.b = -1;
+                ok = mbar_wait(iempty_bar(ii), ((ii / kPaItems) & 1u) ^ 1u);
+                if (!ok) break;
+                ring[ii % kPaItems] = it;
+                mbar_arrive(ifull_bar(ii));
+            }
+        }
+    } else if (warp == 0) {
+        // ---------------- pages: K and V tiles (and steps) ----------------
+        constexpr int NR = I8 ? C::kRaw : NS;
+        const int box = a.box, chunks = kPaTile / box;  // boxes of a tile: lane c loads box c
+        uint32_t n = 0;        // ring places used (K and V in turn)
+        uint32_t flying = 0;   // oldest place that may still be landing
+        uint32_t tile = 0, tile_flying = 0;
+        while (const PaItem* item = take()) {
+            const PaItem it = *item;
+            release();
+            const int end = it.end;
+            auto page_of = [&](int t) {  // this lane's page of tile t, -1 where it has none
+                const int p = t * kPaTile + lane * box;
+                return lane < chunks && t < it.t1 && p < end ? kv_page(a.c, a.b, it.b, p) : -1;
+            };
+            int page = page_of(it.t0);
+            for (int t = it.t0; t < it.t1; ++t, ++tile) {
+                const int page_next = page_of(t + 1);
+                const int slot0 = (t * kPaTile + lane * box) % a.c.page_size;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                if constexpr (I8) {
+                    const int ss = (int)(tile % C::kSteps);
+                    ok = __all_sync(0xffffffffu, mbar_wait(sempty_bar(ss), ((tile / C::kSteps) & 1u) ^ 1u));
+                    if (!ok) break;
+                    tile_flying = tile >= C::kSteps ? tile - C::kSteps + 1 : 0;
+                    if (lane == 0) mbar_arrive_expect_tx(sfull_bar(ss), (uint32_t)(boxes * box * 8));
+                    __syncwarp();
+                    if (page >= 0) {
+                        const uint32_t dst = base + C::kOffStep + (uint32_t)(ss * 2 * kPaTile + lane * box) * 4;
+                        const int64_t off = ((int64_t)page * a.c.kv_heads + it.g) * a.c.page_size + slot0;
+                        bulk_g2s(dst, a.c.k_step + off, (uint32_t)box * 4, sfull_bar(ss));
+                        bulk_g2s(dst + kPaTile * 4, a.c.v_step + off, (uint32_t)box * 4, sfull_bar(ss));
+                    }
+                }
 #pragma unroll
-    for (int e = 0; e < DL; ++e)
-        a.out[t * a.o_stride + h * D + lane * DL + e] = float_to_bf16_bits(end > 0 ? o[e] / l : 0.0f);
+                for (int kv = 0; kv < 2; ++kv, ++n) {
+                    const int st = (int)(n % NR);
+                    const uint32_t fb = I8 ? rfull_bar(st) : full_bar(st), eb = I8 ? rempty_bar(st) : empty_bar(st);
+                    ok = __all_sync(0xffffffffu, mbar_wait(eb, ((n / NR) & 1u) ^ 1u));
+                    if (!ok) break;
+                    flying = n >= NR ? n - NR + 1 : 0;
+                    if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(boxes * box * D * (I8 ? 1 : 2)));
+                    __syncwarp();
+                    if (page >= 0) {
+                        const CUtensorMap* map = kv ? &map_v : &map_k;
+                        if constexpr (I8) {
+                            tma_load_4d(base + C::kOffRaw + st * C::kRawBytes + lane * box * D, map, 0, it.g, slot0, page, fb);
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tma_load_4d(base + C::kOffRing + st * C::kTileBytes + h * C::kHalfBytes + lane * box * 128,
+                                            map, h * 64, it.g, slot0, page, fb);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                page = page_next;
+            }
+            if (!ok) break;
+        }
+        // after a failed wait, let the copies still in flight land first
+        if (!ok && lane == 0) {
+            for (uint32_t j = flying; j < n; ++j)
+                mbar_wait(I8 ? rfull_bar((int)(j % NR)) : full_bar((int)(j % NR)), (j / NR) & 1u);
+            if constexpr (I8)
+                for (uint32_t j = tile_flying; j < tile + 1; ++j) mbar_wait(sfull_bar((int)(j % C::kSteps)), (j / C::kSteps) & 1u);
+        }
+    } else if (warp == 2) {
+        // ---------------- queries: one slot per sub-tile ----------------
+        uint32_t n = 0, flying = 0;
+        while (const PaItem* item = take()) {
+            const int nsub = item->t0 < item->t1 ? item->nsub : 0, row = item->row, g = item->g;
+            release();
+            for (int x = 0; x < nsub; ++x, ++n) {
+                const int st = (int)(n & 1);
+                ok = __all_sync(0xffffffffu, mbar_wait(qempty_bar(st), ((n >> 1) & 1u) ^ 1u));
+                if (!ok) break;
+                flying = n >= 2 ? n - 1 : 0;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(qfull_bar(st), (uint32_t)(a.tokens * a.group * D * 2));
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_4d(base + st * C::kTileBytes + h * C::kHalfBytes, &map_q, h * 64, 0,
+                                    row + x * a.tokens, g, qfull_bar(st));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+        }
+        if (!ok && lane == 0)
+            for (uint32_t j = flying; j < n; ++j) mbar_wait(qfull_bar((int)(j & 1)), (j >> 1) & 1u);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        // Two walks over the tasks: `ahead` issues the scores' products, `behind` the values'.  A group has at most
+        // one task between the two, so the walk ahead is at most two items further on.
+        PaItem* open = reinterpret_cast<PaItem*>(sm + C::kOffOpen);
+        PaTasks ahead(open), behind(open);
+        PaTask q, p;
+        auto advance = [&]() {  // the task after q, from the next item with tiles where its own has none left
+            while (ahead.nsub == 0) {
+                const PaItem* it = take();
+                if (!it) return false;
+                const bool tiles = it->t0 < it->t1;
+                if (tiles && lane == 0) open[ahead.items % kPaItems] = *it;
+                release();
+                if (tiles) ahead.load();
+            }
+            ahead.next(q);
+            return true;
+        };
+        bool have = advance();
+        uint32_t busy = 0;    // bit w: scores issued, their PV not yet
+        uint32_t probs = 0;   // bit w: phase of the group's next probabilities
+        while (ok) {
+            while (have && !((busy >> q.w) & 1u)) {
+                // S = Q K^T
+                const uint32_t kn = 2 * q.tile;
+                const int st = (int)(kn % NS);
+                ok = mbar_wait(qfull_bar((int)(q.slot & 1)), (q.slot >> 1) & 1u) &&
+                     mbar_wait(full_bar(st), (kn / NS) & 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t qd = smem_desc_sw128(base + (q.slot & 1) * C::kTileBytes);
+                    const uint64_t kd = smem_desc_sw128(base + C::kOffRing + st * C::kTileBytes);
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // 16 dimensions (32 bytes) an instruction
+                            const uint64_t o = (uint64_t)((h * C::kHalfBytes + k * 32) >> 4);
+                            tc_mma_f16_ss(tmem + 128u * q.w, qd + o, kd + o, kPaIdescQk, (h | k) != 0);
+                        }
+                    tc_commit(score_bar(q.w));
+                    if (q.frees) tc_commit(empty_bar(st));
+                    if (q.ends) {
+                        tc_commit(qempty_bar((int)(q.slot & 1)));
+                        if (q.nsub == 2) tc_commit(qempty_bar((int)((q.slot + 1) & 1)));
+                    }
+                }
+                __syncwarp();
+                busy |= 1u << q.w;
+                have = advance();
+            }
+            if (!ok) break;
+            if (behind.nsub == 0) {
+                if (behind.items == ahead.items) break;  // the last task is done
+                behind.load();
+            }
+            behind.next(p);
+            // O (+)= P V
+            const uint32_t vn = 2 * p.tile + 1;
+            const int st = (int)(vn % NS);
+            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (vn / NS) & 1u));
+            if (!ok) break;
+            const int ksteps = (p.valid + 15) / 16;
+            if (!I8 && p.fresh && p.valid % 16 != 0) {
+                // values behind the last position that anything sees: zeros (probability zero times whatever
+                // the page holds there would not be)
+                uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes;
+                for (int e = lane; e < (16 * ksteps - p.valid) * C::kHalves * 8; e += 32) {
+                    const int h = e / ((16 * ksteps - p.valid) * 8), r = p.valid + (e / 8) % (16 * ksteps - p.valid);
+                    *reinterpret_cast<uint4*>(vt + h * C::kHalfBytes + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            ok = __all_sync(0xffffffffu, mbar_wait(prob_bar(p.w), (probs >> p.w) & 1u));
+            if (!ok) break;
+            probs ^= 1u << p.w;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint64_t vd = pa_desc_v(base + C::kOffRing + st * C::kTileBytes, C::kHalfBytes);
+                for (int k = 0; k < ksteps; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
+                    tc_mma_f16_ts(tmem + 256u + 128u * p.w, tmem + 128u * p.w + 8u * k, vd + (uint64_t)(k * 2048 >> 4),
+                                  pa_idesc_pv<D>(), !p.first || k != 0);
+                if (p.frees) tc_commit(empty_bar(st));
+                if (p.last) tc_commit(odone_bar(p.w));
+            }
+            __syncwarp();
+            busy &= ~(1u << p.w);
+        }
+        // every MMA this thread issued has finished before TMEM is freed
+        if (lane == 0) {
+            tc_commit(drain_bar);
+            mbar_wait(drain_bar, 0);
+        }
+        __syncwarp();
+    }
+    } else if (warp >= 12) {
+        // ---------------- int8 codes -> bf16 operand tiles ----------------
+        if constexpr (I8) {
+            setmaxnreg_dec<C::kRegsConv>();
+            const int th = threadIdx.x - 384;
+            uint32_t n = 0;
+            while (const PaItem* item = take()) {
+                const int parts = 2 * (item->t1 - item->t0);  // K and V of each tile
+                release();
+                for (int x = 0; x < parts; ++x, ++n) {
+                    const int rs = (int)(n % C::kRaw), st = (int)(n % NS);
+                    const bool got = mbar_wait(rfull_bar(rs), (n / C::kRaw) & 1u) &&
+                                     mbar_wait(empty_bar(st), ((n / NS) & 1u) ^ 1u);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    const uint8_t* src = sm + C::kOffRaw + rs * C::kRawBytes;
+                    uint8_t* dst = sm + C::kOffRing + st * C::kTileBytes;
+#pragma unroll 4
+                    for (int e = th; e < kPaTile * D / 16; e += 128) {
+                        const int r = e / (D / 16), ch = e % (D / 16);  // row, run of 16 codes
+                        const uint4 w = *reinterpret_cast<const uint4*>(src + r * D + ch * 16);
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                // a code c in two's complement is m - 128 s (m: low 7 bits, s: sign): as bf16,
+                                // (128 + m) - (128 + 128 s), each term and the difference exact
+                                const uint32_t t = __byte_perm(ws[i], 0, y ? 0x4342 : 0x4140);
+                                const uint32_t m = (t & 0x007F007Fu) | 0x43004300u, s = (t & 0x00800080u) | 0x43004300u;
+                                const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                                                 *reinterpret_cast<const __nv_bfloat162*>(&s));
+                                o[2 * i + y] = *reinterpret_cast<const uint32_t*>(&d);
+                            }
+                        uint8_t* half = dst + (ch >> 2) * C::kHalfBytes;
+                        *reinterpret_cast<uint4*>(half + sw128_offset(r, (ch & 3) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(half + sw128_offset(r, (ch & 3) * 2 + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async_smem();  // generic writes -> visible to the tensor core
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(full_bar(st));
+                        mbar_arrive(rempty_bar(rs));
+                    }
+                }
+                if (!ok) break;
+            }
+        }
+    } else {
+        // ---------------- softmax: a row per thread ----------------
+        setmaxnreg_inc<C::kRegsSoft>();
+        const int w = (warp - 4) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const int tok = row / a.group, hh = row % a.group;
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const uint32_t ts = tmem + lanes + 128u * w, to = tmem + lanes + 256u + 128u * w;
+        float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
+        uint32_t seen = 0, done = 0, merges = 0, tile = 0;
+        int state = 0;      // of this CTA's first share (see desc)
+        int4 began = make_int4(0, 0, 0, 0);
+        while (const PaItem* item = take()) {
+            const bool pair = item->nsub == 2;
+            const int t0 = item->t0, t1 = item->t1;
+            const int sub = pair ? w : 0;  // this group's sub-tile of the item
+            const int tokens = min(a.tokens, item->tokens - sub * a.tokens);
+            const bool live = tok < tokens;
+            const bool warp_live = quad * 32 < tokens * a.group;
+            // positions that this row sees
+            const int vend = !live ? 0 : a.causal ? min(max(item->vend + sub * a.tokens + tok, 0), item->len) : item->len;
+            const int t_end = pair && w == 0 ? item->nt0 : t1;
+            float m = -INFINITY, l = 0.0f;
+            bool first = true;
+            for (int t = t0; t < t1; ++t, ++tile) {
+                const bool mine = pair ? t < t_end : ((t - t0) & 1) == w;
+                const float* ks = nullptr;
+                if constexpr (I8) {  // a tile of the other group's too: the ring's phases go by both
+                    const int ss = (int)(tile % C::kSteps);
+                    ok = __all_sync(0xffffffffu, mbar_wait(sfull_bar(ss), (tile / C::kSteps) & 1u));
+                    if (!ok) break;
+                    ks = reinterpret_cast<const float*>(sm + C::kOffStep) + ss * 2 * kPaTile;
+                }
+                if (mine) {
+                    const bool got = mbar_wait(score_bar(w), seen & 1u);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    ++seen;
+                    tc_fence_after();
+                }
+                if (mine && warp_live) {
+                    float s[kPaTile];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32u * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+                    tmem_ld_wait();
+                    if constexpr (I8) {
+#pragma unroll
+                        for (int c = 0; c < kPaTile; c += 4) {
+                            const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
+                            mul2(s[c], s[c + 1], k4.x, k4.y);
+                            mul2(s[c + 2], s[c + 3], k4.z, k4.w);
+                        }
+                    }
+                    const int vis = vend - t * kPaTile;  // columns that this row sees
+                    const bool masked = __any_sync(0xffffffffu, vis < kPaTile);
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < kPaTile; ++c)
+                            if (c >= vis) s[c] = -INFINITY;
+                    }
+                    float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+                    for (int c = 4; c < kPaTile; c += 4) {
+                        x0 = fmaxf(x0, s[c]);
+                        x1 = fmaxf(x1, s[c + 1]);
+                        x2 = fmaxf(x2, s[c + 2]);
+                        x3 = fmaxf(x3, s[c + 3]);
+                    }
+                    const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+                    if (first) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, (top - m) * a.qscale > kPaMaxGrowth)) {
+                        const float mn = fmaxf(m, top);
+                        const float alpha = m == mn ? 1.0f : ex2((m - mn) * a.qscale);
+                        m = mn;
+                        l *= alpha;
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c, o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st32(to + c, o);
+                        }
+                    }
+                    first = false;
+                    const float off = m == -INFINITY ? 0.0f : -m * a.qscale;
+                    float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < kPaTile; c += 2) {
+                        fma2(s[c], s[c + 1], a.qscale, a.qscale, off, off);
+                        s[c] = ex2(s[c]);
+                        s[c + 1] = ex2(s[c + 1]);
+                        add2(l0, l1, s[c], s[c + 1]);
+                    }
+                    l += l0 + l1;
+                    if constexpr (I8) {
+                        const float* vs = ks + kPaTile;
+#pragma unroll
+                        for (int c = 0; c < kPaTile; c += 4) {
+                            const float4 v4 = *reinterpret_cast<const float4*>(vs + c);
+                            mul2(s[c], s[c + 1], v4.x, v4.y);
+                            mul2(s[c + 2], s[c + 3], v4.z, v4.w);
+                        }
+                        if (masked) {  // a step behind the last position may be anything
+#pragma unroll
+                            for (int c = 0; c < kPaTile; ++c)
+                                if (c >= vis) s[c] = 0.0f;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]);
+                        tmem_st16(ts + 16u * c, pk);
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (I8) mbar_arrive(sempty_bar((int)(tile % C::kSteps)));
+                    if (mine) mbar_arrive(prob_bar(w));
+                }
+            }
+            if (!ok) break;
+            // ---- the rows' results over [t0, t1) ----
+            const int mine_tiles = pair ? max(t_end - t0, 0) : (t1 - t0 + 1 - w) / 2;
+            if (mine_tiles > 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(odone_bar(w), done & 1u));
+                if (!ok) break;
+                ++done;
+                tc_fence_after();
+            }
+            const bool whole = t0 == 0 && t1 == item->nt;
+            const bool merge = !pair && t1 - t0 > 1;
+            float f0 = 1.0f, f1 = 0.0f;
+            if (merge && w == 1) {
+                ml[row] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(mfull_bar);
+            }
+            if (merge && w == 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(mfull_bar, merges & 1u));
+                if (!ok) break;
+                tc_fence_after();
+                const float2 other = ml[row];
+                const float mn = fmaxf(m, other.x);
+                f0 = m == mn ? 1.0f : ex2((m - mn) * a.qscale);
+                f1 = other.x == mn ? 1.0f : ex2((other.x - mn) * a.qscale);
+                m = mn;
+                l = l * f0 + other.y * f1;
+            }
+            if ((pair || w == 0) && warp_live) {
+                const int r_item = sub * kPaRows + row;
+                const int slot = t0 == 0 ? 1 : 0;
+                const int64_t prow = ((int64_t)blockIdx.x * 2 + slot) * a.part_rows + r_item;
+                uint16_t* orow = a.out + (int64_t)(item->row + sub * a.tokens + tok) * a.o_stride +
+                                 (int64_t)(item->g * a.group + hh) * D;
+                const float inv = 1.0f / l;
+                float poison = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    if (mine_tiles > 0) {
+                        tmem_ld32(to + c, o);
+                        if (merge) {
+                            uint32_t o1[32];
+                            tmem_ld32(to + 128u + c, o1);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e]) * f0));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) poison = fmaf(__uint_as_float(o[e]), 0.0f, poison);
+                    if (live && whole) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = vend > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4*>(orow + c + 8 * e) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(a.part + prow * D + c + 4 * e) =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    __syncwarp();
+                }
+                if (live && !whole)
+                    *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m == -INFINITY ? m : m * a.qscale, l);
+                if constexpr (!I8) {
+                    // an infinity or NaN came out.  Where it stands in a position that the row does not see (its
+                    // probability there is zero, the product is not), the row is computed from what it sees alone
+                    uint32_t bad = __ballot_sync(0xffffffffu, live && !(poison == 0.0f));
+                    __syncwarp();
+                    while (bad) {
+                        const int src = __ffs(bad) - 1;
+                        bad &= bad - 1;
+                        const int r2 = quad * 32 + src, tok2 = r2 / a.group, hh2 = r2 % a.group;
+                        const int vend2 = __shfl_sync(0xffffffffu, vend, src);
+                        const int64_t token = item->row + sub * a.tokens + tok2;
+                        const int64_t head = item->g * a.group + hh2;
+                        float o[D / 32], m2, l2;
+                        pa_row<D>(a, item->b, item->g, a.q + token * a.q_stride + head * D, t0 * kPaTile,
+                                  min(vend2, t1 * kPaTile), o, &m2, &l2);
+                        const int64_t prow2 = ((int64_t)blockIdx.x * 2 + slot) * a.part_rows + sub * kPaRows + r2;
+#pragma unroll
+                        for (int e = 0; e < D / 32; ++e) {
+                            if (whole)
+                                a.out[token * a.o_stride + head * D + lane * (D / 32) + e] =
+                                    float_to_bf16_bits(vend2 > 0 ? o[e] / l2 : 0.0f);
+                            else
+                                a.part[prow2 * D + lane * (D / 32) + e] = o[e];
+                        }
+                        if (!whole && lane == 0) *reinterpret_cast<float2*>(a.part_ml + prow2 * 2) = make_float2(m2, l2);
+                    }
+                }
+            }
+            if (merge) {
+                tc_fence_before();
+                __syncwarp();
+                if (w == 0) {
+                    if (lane == 0) mbar_arrive(mempty_bar);
+                } else {
+                    ok = __all_sync(0xffffffffu, mbar_wait(mempty_bar, merges & 1u));
+                }
+                ++merges;
+            }
+            if (!whole) {
+                if (t0 == 0)
+                    began = make_int4(item->tokens, item->row, item->g, item->vend);
+                else
+                    state = t1 == item->nt ? 2 : 1;
+            }
+            if (!ok) break;
+            release();
+        }
+        if (w == 0 && quad == 0 && lane == 0) {
+            a.desc[2 * blockIdx.x] = make_int4(state, 0, 0, 0);
+            a.desc[2 * blockIdx.x + 1] = began;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---- merging the parts of items cut by shares ----------------------------------
+// CTA (c, y): the item that began in CTA c of the attention kernel and did not
+// end there, rows y, y + gridDim.y, ... by warp: its parts lie in CTA c and
+// the following ones up to the first that ends it, merged in that order,
+//   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
+constexpr int kPaMergeThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kPaMergeThreads) attn_merge_kernel(const PagedAttnArgs a, int grid) {
+    constexpr int DL = D / 32;
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int4 it = __ldcg(a.desc + 2 * c + 1);
+    if (it.x == 0) return;
+    const int nsub = it.x > a.tokens ? 2 : 1;
+    const int rows0 = min(it.x, a.tokens) * a.group, rows1 = (it.x - min(it.x, a.tokens)) * a.group;
+    // the last CTA with a part of the item
+    int last = grid - 1;
+    for (int x = c + 1; x < grid; x += 32) {
+        const bool ends = x + lane < grid && __ldcg(&a.desc[2 * (x + lane)].x) == 2;
+        const uint32_t hit = __ballot_sync(0xffffffffu, ends);
+        if (hit) {
+            last = x + __ffs(hit) - 1;
+            break;
+        }
+    }
+    for (int r = blockIdx.y * (kPaMergeThreads / 32) + warp; r < rows0 + rows1; r += gridDim.y * (kPaMergeThreads / 32)) {
+        const int sub = r < rows0 ? 0 : 1, rr = sub ? r - rows0 : r;
+        const int64_t prow = (nsub == 2 ? sub * kPaRows : 0) + rr;
+        const int tok = sub * a.tokens + rr / a.group, hh = rr % a.group;
+        auto part_of = [&](int x) { return ((int64_t)x * 2 + (x == c ? 1 : 0)) * a.part_rows + prow; };
+        auto present = [&](int x) { return x <= last && (x == c || __ldcg(&a.desc[2 * x].x) != 0); };
+        float mx = -INFINITY;
+        for (int x = c; x <= last; x += 32)
+            if (present(x + lane)) mx = fmaxf(mx, __ldcg(a.part_ml + part_of(x + lane) * 2));
+        mx = warp_max_f(mx);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        float den = 0.0f, num[DL] = {};
+        for (int x0 = c; x0 <= last; x0 += 32) {
+            float f = 0.0f, fl = 0.0f;
+            if (present(x0 + lane)) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + part_of(x0 + lane) * 2));
+                f = v.x == mx && mx != -INFINITY ? 1.0f : exp2f(v.x - ref);
+                fl = f * v.y;
+            }
+            const uint32_t some = __ballot_sync(0xffffffffu, present(x0 + lane));
+            den += warp_sum_f(fl);
+#pragma unroll 8
+            for (int i = 0; i < 32; ++i) {
+                if (!((some >> i) & 1)) continue;
+                const float fi = __shfl_sync(0xffffffffu, f, i);
+                const float* src = a.part + part_of(x0 + i) * D + lane * DL;
+                if constexpr (DL == 4) {
+                    const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
+                    num[0] = fmaf(fi, o.x, num[0]);
+                    num[1] = fmaf(fi, o.y, num[1]);
+                    num[2] = fmaf(fi, o.z, num[2]);
+                    num[3] = fmaf(fi, o.w, num[3]);
+                } else {
+                    const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
+                    num[0] = fmaf(fi, o.x, num[0]);
+                    num[1] = fmaf(fi, o.y, num[1]);
+                }
+            }
+        }
+        const int vend = a.causal ? it.w + tok : it.w;
+        uint16_t* dst = a.out + (int64_t)(it.y + tok) * a.o_stride + (int64_t)(it.z * a.group + hh) * D + lane * DL;
+#pragma unroll
+        for (int e = 0; e < DL; ++e) dst[e] = float_to_bf16_bits(vend > 0 ? num[e] / den : 0.0f);
+    }
 }
 
 }  // namespace bl

@@ -803,7 +803,9 @@ bl_status kv_check(const bl_kv_cache* c, const bl_kv_batch* b, int64_t T, KvCach
     if (c->num_pages <= 0 || c->num_pages > INT32_MAX || c->page_size <= 0 || c->page_size % 16 != 0 ||
         c->page_size > (1 << 20) || c->kv_heads <= 0 || c->kv_heads > 65535)
         return BL_ERR_SHAPE;
-    if (b->batch < 0 || b->batch >= INT32_MAX || b->max_pages < 0 || b->max_pages > INT32_MAX) return BL_ERR_SHAPE;
+    if (b->batch < 0 || b->batch >= INT32_MAX || b->max_pages < 0 ||
+        b->max_pages > kKvMaxPositions / c->page_size)
+        return BL_ERR_SHAPE;
     if (T < 0 || T > INT32_MAX / c->kv_heads) return BL_ERR_SHAPE;
     const int64_t unit = i8 ? 16 : 8, most = ((int64_t)1 << 40) / (i8 ? 1 : 2);
     for (const int64_t s : {c->stride_page, c->stride_slot, c->stride_head}) {
@@ -830,7 +832,7 @@ bl_status kv_check(const bl_kv_cache* c, const bl_kv_batch* b, int64_t T, KvCach
     ba->batch = (int)b->batch;
     ba->max_pages = (int)b->max_pages;
     ba->T = (int)T;
-    ba->max_len = (int)std::min<int64_t>(b->max_pages * c->page_size, INT32_MAX);
+    ba->max_len = (int)(b->max_pages * c->page_size);
     return BL_OK;
 }
 
@@ -853,10 +855,77 @@ bl_status attn_paged_check(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t
     return T < 0 || T > INT32_MAX / q_heads ? BL_ERR_SHAPE : BL_OK;
 }
 
+// 4-D tensor (innermost contiguous), elements of elem_bytes; strides in elements.
+bool make_map_4d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes, const void* ptr,
+                 const int64_t (&dims)[4], const int64_t (&strides)[3], const int (&box)[4],
+                 CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) {
+        snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled is unavailable");
+        return false;
+    }
+    cuuint64_t d[4], st[3];
+    cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) {
+        d[i] = (cuuint64_t)dims[i];
+        bx[i] = (cuuint32_t)box[i];
+        if (i < 3) st[i] = (cuuint64_t)(strides[i] * elem_bytes);
+    }
+    const CUresult r = fn(map, type, 4, const_cast<void*>(ptr), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+        return false;
+    }
+    return true;
+}
+
+// Layout of bitlinear_attn_paged's workspace: a description per CTA, then the
+// partial (max, sum) pairs and vectors of up to two cut items per CTA.
+struct PagedWs {
+    int64_t part_rows, desc_bytes, ml_bytes, bytes;
+};
+PagedWs attn_paged_ws(int64_t T, int64_t group, int64_t head_dim, int sms) {
+    const int64_t tokens = kPaRows / group;
+    PagedWs w;
+    w.part_rows = T <= tokens ? T * group : 2 * kPaRows;  // rows of an item: one sub-tile, or two
+    w.desc_bytes = ((int64_t)sms * 2 * sizeof(int4) + 255) / 256 * 256;
+    w.ml_bytes = ((int64_t)sms * 2 * w.part_rows * 8 + 255) / 256 * 256;
+    w.bytes = w.desc_bytes + w.ml_bytes + (int64_t)sms * 2 * w.part_rows * head_dim * 4;
+    return w;
+}
+
 template <int D, bool I8>
-bl_status attn_paged_launch(const PagedAttnArgs& a, cudaStream_t stream) {
-    const int64_t warps = (int64_t)a.b.T * a.heads;
-    return launch(attn_paged_row_kernel<D, I8>, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, a);
+bl_status attn_paged_launch(PagedAttnArgs& a, void* workspace, int dev, const DeviceInfo& info,
+                            cudaStream_t stream) {
+    const PagedWs w = attn_paged_ws(a.b.T, a.group, D, info.sms);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.desc = reinterpret_cast<int4*>(ws);
+    a.part_ml = reinterpret_cast<float*>(ws + w.desc_bytes);
+    a.part = reinterpret_cast<float*>(ws + w.desc_bytes + w.ml_bytes);
+    a.part_rows = (int)w.part_rows;
+    a.tokens = kPaRows / a.group;
+    a.box = kPaTile;
+    while (a.c.page_size % a.box != 0) a.box /= 2;
+    CUtensorMap map_q, map_k, map_v;
+    const int64_t qd[4] = {D, a.group, a.b.T, a.c.kv_heads}, qs[3] = {D, a.q_stride, (int64_t)a.group * D};
+    const int qb[4] = {64, a.group, a.tokens, 1};
+    const int64_t kd[4] = {D, a.c.kv_heads, a.c.page_size, a.c.num_pages}, ks[3] = {a.c.sh, a.c.ss, a.c.sp};
+    const int kb[4] = {I8 ? D : 64, 1, a.box, 1};
+    const CUtensorMapDataType kt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const CUtensorMapSwizzle sw = I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_map_4d(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw) ||
+        !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw))
+        return BL_ERR_CUDA;
+    using C = PaCfg<D, I8>;
+    if (prepare_kernel(reinterpret_cast<const void*>(attn_paged_kernel<D, I8>), dev, info, C::kThreads, C::kSmem) < 0)
+        return BL_ERR_CUDA;
+    const bl_status st = launch(attn_paged_kernel<D, I8>, dim3((unsigned)info.sms), dim3(C::kThreads), (size_t)C::kSmem,
+                                stream, map_q, map_k, map_v, (const PagedAttnArgs&)a);
+    if (st != BL_OK) return st;
+    return launch(attn_merge_kernel<D>, dim3((unsigned)info.sms, 4), dim3(kPaMergeThreads), 0, stream,
+                  (const PagedAttnArgs&)a, info.sms);
 }
 
 }  // namespace
@@ -1343,7 +1412,10 @@ bl_status bitlinear_attn_paged_workspace_size(int64_t T, int64_t q_heads, int64_
     if (!bytes) return BL_ERR_NULL;
     bl_status st;
     if ((st = attn_paged_check(T, q_heads, kv_heads, head_dim)) != BL_OK) return st;
-    *bytes = 0;
+    int dev;
+    DeviceInfo info;
+    if ((st = current_device(&dev, &info)) != BL_OK) return st;
+    *bytes = (size_t)attn_paged_ws(T, q_heads / kv_heads, head_dim, info.sms).bytes;
     return BL_OK;
 }
 
@@ -1363,6 +1435,9 @@ bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batc
     int dev;
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != BL_OK) return st;
+    if (!workspace || !aligned16(workspace) ||
+        workspace_bytes < (size_t)attn_paged_ws(T, q_heads / cache->kv_heads, cache->head_dim, info.sms).bytes)
+        return BL_ERR_WORKSPACE;
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;
@@ -1372,9 +1447,10 @@ bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batc
     a.causal = causal != 0;
     a.qscale = scale * kLog2e;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cache->format == BL_KV_I8)
-        return cache->head_dim == 128 ? attn_paged_launch<128, true>(a, s) : attn_paged_launch<64, true>(a, s);
-    return cache->head_dim == 128 ? attn_paged_launch<128, false>(a, s) : attn_paged_launch<64, false>(a, s);
+    auto run = cache->head_dim == 128
+                   ? (cache->format == BL_KV_I8 ? attn_paged_launch<128, true> : attn_paged_launch<128, false>)
+                   : (cache->format == BL_KV_I8 ? attn_paged_launch<64, true> : attn_paged_launch<64, false>);
+    return run(a, workspace, dev, info, s);
 }
 
 bl_status bitlinear_device_status(void* stream) {

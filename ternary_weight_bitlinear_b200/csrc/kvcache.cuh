@@ -26,6 +26,7 @@
 namespace bl {
 
 constexpr int kKvThreads = 128;
+constexpr int64_t kKvMaxPositions = 1 << 30;  // of a page table's row: position arithmetic stays in 32 bits
 
 struct KvCacheArgs {
     void* k;                     // bf16 or int8 pages
@@ -43,7 +44,7 @@ struct KvBatchArgs {
     int batch;
     int max_pages;
     int T;                       // rows the caller's buffers have
-    int max_len;                 // max_pages * page_size, at most INT32_MAX
+    int max_len;                 // max_pages * page_size, at most kKvMaxPositions
 };
 
 // A sequence as the kernels see it: whatever the arrays hold, the rows lie

@@ -48,6 +48,7 @@ BAD = [
     ({}, dict(batch=-1), SHAPE),
     ({}, dict(batch=2 ** 31), SHAPE),
     ({}, dict(max_pages=-1), SHAPE),
+    ({}, dict(max_pages=2 ** 26 + 1), SHAPE),
     ({}, dict(cu_q=None), NULL),
     ({}, dict(kv_len=None), NULL),
     ({}, dict(pages=None), NULL),

@@ -49,6 +49,7 @@ namespace bl {
 constexpr int kPaRows = 128;     // rows of a sub-tile (MMA M)
 constexpr int kPaTile = 128;     // positions of a tile
 constexpr int kPaItemUnits = 1;  // cost of an item beside its tiles, in tiles of one sub-tile
+constexpr int kNoMask = 1 << 30;
 constexpr float kPaMaxGrowth = 8.0f;  // log2 growth of the maximum that a row's sums absorb
 
 struct PagedAttnArgs {
@@ -90,7 +91,9 @@ struct PaItem {
     int end;         // positions that some row of the item sees
     int vend;        // positions that its first token sees; below zero where it has no place
     int len;         // positions of the sequence
-    int pad[4];
+    int slot;        // running number of its first Q tile; a pair whose first sub-tile has no tile here loads the
+    int nq;          // second only (nq of them, 0 without tiles)
+    int pad[2];
 };
 constexpr int kPaItems = 4;      // ring of items
 
@@ -120,6 +123,7 @@ struct PaWalk {
     int b, g, i;         // current item: sequence, head, index within (sequence, head)
     KvSeq s;
     int items;           // items per head of the sequence
+    int slot = 0;        // Q tiles so far
 
     __device__ __forceinline__ PaWalk(const PagedAttnArgs& args, const int64_t* plan) : a(args) {
         u0 = plan[0];
@@ -154,6 +158,9 @@ struct PaWalk {
             it.end = pa_end(a, s, first + it.tokens);
             it.vend = a.causal ? s.len - s.n + first + 1 : s.len;
             it.len = s.len;
+            it.nq = lo == hi ? 0 : nsub == 2 && it.nt0 > lo ? 2 : 1;
+            it.slot = slot;
+            slot += it.nq;
             const bool mine = lo < hi || (nt == 0 && from <= 0);
             at += c;
             if (++i == items) {
@@ -276,11 +283,10 @@ struct PaCfg {
     static constexpr int kOffStep = kOffRaw + kRaw * kRawBytes;
     static constexpr int kOffMl = kOffStep + kSteps * 2 * kPaTile * 4;  // second group's (max, sum)
     static constexpr int kOffItems = kOffMl + kPaRows * 8;
-    static constexpr int kOffOpen = kOffItems + kPaItems * (int)sizeof(PaItem);  // the MMA issuer's own
-    static constexpr int kOffBar = kOffOpen + kPaItems * (int)sizeof(PaItem);
+    static constexpr int kOffBar = kOffItems + kPaItems * (int)sizeof(PaItem);
     // barriers: operand ring full/empty, raw full/empty, steps full/empty, Q full/empty,
     // scores, probabilities, output done (one per group), merge full/empty, drain, items full/empty
-    static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kSteps + 4 + 6 + 2 + 1 + 2 * kPaItems;
+    static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kSteps + 4 + 6 + 2 + 2 + 2 * kPaItems;
     static constexpr int kOffPlan = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffPlan + 256 + 1024;       // plan words, alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -386,73 +392,6 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
         : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
 }
 
-// ---- the tasks of a CTA: (softmax group, position tile) in tensor-core order ----
-struct PaTask {
-    int w;             // softmax group
-    int t;             // position tile
-    int valid;         // positions of the tile that some row of the item sees
-    uint32_t tile;     // running number of the tile (its K and V ring places)
-    uint32_t slot;     // running number of the Q sub-tile
-    bool first, last;  // of this group in the item
-    bool frees;        // last task of the tile
-    bool ends;         // last task of the item
-    bool fresh;        // first task of the tile
-    int nsub;
-};
-
-struct PaTasks {
-    PaItem* open;         // items with tiles, kPaItems places: filled by the walk ahead, read by the one behind
-    uint32_t items, tile, slot;  // items opened, tiles and Q sub-tiles passed
-    int t, t0, t1, w, end, nt0, nsub;   // nsub 0: no item open
-    __device__ __forceinline__ explicit PaTasks(PaItem* o)
-        : open(o), items(0), tile(0), slot(0), t(0), t0(0), t1(0), w(0), end(0), nt0(0), nsub(0) {}
-    __device__ __forceinline__ void load() {
-        const PaItem& it = open[items++ % kPaItems];
-        t0 = t = it.t0;
-        t1 = it.t1;
-        nsub = it.nsub;
-        end = it.end;
-        nt0 = it.nt0;
-        w = nsub == 2 && t >= nt0 ? 1 : 0;
-    }
-    // The next task of the open item.
-    __device__ __forceinline__ void next(PaTask& k) {
-        k.t = t;
-        k.valid = min(kPaTile, end - t * kPaTile);
-        k.tile = tile;
-        k.nsub = nsub;
-        k.ends = false;
-        if (nsub == 2) {
-            k.w = w;
-            k.slot = slot + w;
-            k.first = t == t0;
-            k.last = t == (w == 0 ? nt0 : t1) - 1;
-            k.frees = w == 1;
-            k.fresh = w == 0 || t >= nt0;
-            if (w == 1) {
-                ++t;
-                ++tile;
-                w = t < nt0 ? 0 : 1;
-            } else {
-                w = 1;
-            }
-        } else {
-            k.w = (t - t0) & 1;
-            k.slot = slot;
-            k.first = t - t0 < 2;
-            k.last = t + 2 >= t1;
-            k.frees = k.fresh = true;
-            ++t;
-            ++tile;
-        }
-        if (t == t1) {
-            k.ends = true;
-            slot += nsub;
-            nsub = 0;
-        }
-    }
-};
-
 // ---- one row by a warp, position by position --------------------------------
 // The (max, sum, vector) of one row over positions [j0, j1) straight from the
 // cache, D/32 dimensions a lane, bf16 pages: only the positions that the row
@@ -516,11 +455,11 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     auto prob_bar = [&](int w) { return bars + 8u * (kB2 + 6 + w); };
     auto odone_bar = [&](int w) { return bars + 8u * (kB2 + 8 + w); };
     const uint32_t mfull_bar = bars + 8u * (kB2 + 10), mempty_bar = bars + 8u * (kB2 + 11);
-    const uint32_t drain_bar = bars + 8u * (kB2 + 12);
-    const uint32_t item_bars = bars + 8u * (kB2 + 13);  // full, then empty
+    auto drain_bar = [&](int w) { return bars + 8u * (kB2 + 12 + w); };
+    const uint32_t item_bars = bars + 8u * (kB2 + 14);  // full, then empty
     auto ifull_bar = [&](uint32_t i) { return item_bars + 8u * (i % kPaItems); };
     auto iempty_bar = [&](uint32_t i) { return item_bars + 8u * (kPaItems + i % kPaItems); };
-    static_assert(kB2 + 13 + 2 * kPaItems == C::kBars, "barrier count");
+    static_assert(kB2 + 14 + 2 * kPaItems == C::kBars, "barrier count");
     PaItem* ring = reinterpret_cast<PaItem*>(sm + C::kOffItems);
     int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // 6 words
     int64_t* warp_sums = plan + 8;                                      // 16 words
@@ -530,7 +469,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
             mbar_init(full_bar(s), I8 ? 4 : 1);  // converter warps, or the loader's expect
-            mbar_init(empty_bar(s), 1);
+            mbar_init(empty_bar(s), 2);          // one by each group
         }
         for (int s = 0; s < C::kRaw; ++s) {
             mbar_init(rfull_bar(s), 1);
@@ -542,17 +481,17 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(qfull_bar(s), 1);
-            mbar_init(qempty_bar(s), 1);
+            mbar_init(qempty_bar(s), 2);
             mbar_init(score_bar(s), 1);
             mbar_init(prob_bar(s), 4);
             mbar_init(odone_bar(s), 1);
+            mbar_init(drain_bar(s), 1);
         }
         mbar_init(mfull_bar, 4);
         mbar_init(mempty_bar, 4);
-        mbar_init(drain_bar, 1);
         for (int i = 0; i < kPaItems; ++i) {
             mbar_init(ifull_bar(i), 1);
-            mbar_init(iempty_bar(i), I8 ? 15 : 11);  // loaders, MMA issuer, softmax (and converter) warps
+            mbar_init(iempty_bar(i), I8 ? 15 : 11);  // page loader, MMA issuers, softmax (and converter) warps
         }
         mbar_init_fence();
     }
@@ -583,18 +522,35 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     if (warp < 4) {
     setmaxnreg_dec<C::kRegsRest>();
     if (warp == 3) {
-        // ---------------- scheduler ----------------
+        // ---------------- scheduler, and the queries: one slot per sub-tile ----------------
         if (lane == 0) {
             PaWalk walk(a, plan);
             PaItem it;
+            uint32_t n = 0, flying = 0;
             for (bool more = true; more && ok; ++ii) {
                 more = walk.next(it);
-                if (!more) it.b = -1;
+                if (!more) {
+                    it.b = -1;
+                    it.nq = 0;
+                }
                 ok = mbar_wait(iempty_bar(ii), ((ii / kPaItems) & 1u) ^ 1u);
                 if (!ok) break;
                 ring[ii % kPaItems] = it;
                 mbar_arrive(ifull_bar(ii));
+                for (int x = 0; x < it.nq; ++x, ++n) {
+                    const int st = (int)(n & 1);
+                    ok = mbar_wait(qempty_bar(st), ((n >> 1) & 1u) ^ 1u);
+                    if (!ok) break;
+                    flying = n >= 2 ? n - 1 : 0;
+                    mbar_arrive_expect_tx(qfull_bar(st), (uint32_t)(a.tokens * a.group * D * 2));
+#pragma unroll
+                    for (int h = 0; h < C::kHalves; ++h)
+                        tma_load_4d(base + st * C::kTileBytes + h * C::kHalfBytes, &map_q, h * 64, 0,
+                                    it.row + (it.nsub - it.nq + x) * a.tokens, it.g, qfull_bar(st));
+                }
             }
+            if (!ok)
+                for (uint32_t j = flying; j < n; ++j) mbar_wait(qfull_bar((int)(j & 1)), (j >> 1) & 1u);
         }
     } else if (warp == 0) {
         // ---------------- pages: K and V tiles (and steps) ----------------
@@ -664,125 +620,90 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             if constexpr (I8)
                 for (uint32_t j = tile_flying; j < tile + 1; ++j) mbar_wait(sfull_bar((int)(j % C::kSteps)), (j / C::kSteps) & 1u);
         }
-    } else if (warp == 2) {
-        // ---------------- queries: one slot per sub-tile ----------------
-        uint32_t n = 0, flying = 0;
-        while (const PaItem* item = take()) {
-            const int nsub = item->t0 < item->t1 ? item->nsub : 0, row = item->row, g = item->g;
-            release();
-            for (int x = 0; x < nsub; ++x, ++n) {
-                const int st = (int)(n & 1);
-                ok = __all_sync(0xffffffffu, mbar_wait(qempty_bar(st), ((n >> 1) & 1u) ^ 1u));
-                if (!ok) break;
-                flying = n >= 2 ? n - 1 : 0;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(qfull_bar(st), (uint32_t)(a.tokens * a.group * D * 2));
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tma_load_4d(base + st * C::kTileBytes + h * C::kHalfBytes, &map_q, h * 64, 0,
-                                    row + x * a.tokens, g, qfull_bar(st));
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
-        }
-        if (!ok && lane == 0)
-            for (uint32_t j = flying; j < n; ++j) mbar_wait(qfull_bar((int)(j & 1)), (j >> 1) & 1u);
-    } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        // Two walks over the tasks: `ahead` issues the scores' products, `behind` the values'.  A group has at most
-        // one task between the two, so the walk ahead is at most two items further on.
-        PaItem* open = reinterpret_cast<PaItem*>(sm + C::kOffOpen);
-        PaTasks ahead(open), behind(open);
-        PaTask q, p;
-        auto advance = [&]() {  // the task after q, from the next item with tiles where its own has none left
-            while (ahead.nsub == 0) {
-                const PaItem* it = take();
-                if (!it) return false;
-                const bool tiles = it->t0 < it->t1;
-                if (tiles && lane == 0) open[ahead.items % kPaItems] = *it;
-                release();
-                if (tiles) ahead.load();
-            }
-            ahead.next(q);
-            return true;
-        };
-        bool have = advance();
-        uint32_t busy = 0;    // bit w: scores issued, their PV not yet
-        uint32_t probs = 0;   // bit w: phase of the group's next probabilities
-        while (ok) {
-            while (have && !((busy >> q.w) & 1u)) {
-                // S = Q K^T
-                const uint32_t kn = 2 * q.tile;
-                const int st = (int)(kn % NS);
-                ok = mbar_wait(qfull_bar((int)(q.slot & 1)), (q.slot >> 1) & 1u) &&
-                     mbar_wait(full_bar(st), (kn / NS) & 1u);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+    } else {
+        // ---------------- MMA issuers: warp 1 + w for softmax group w ----------------
+        // In order: P V of the group's last tile (once its probabilities are there), then Q K^T of its next one into
+        // the same columns.  The two groups' chains fill each other's gaps on the tensor core.
+        const int w = warp - 1;
+        if (lane == 0) {
+            const uint32_t sc = tmem + 128u * w, oc = tmem + 256u + 128u * w;
+            uint32_t n = 0, probs = 0;   // ring fills passed, probabilities waited for
+            struct { int st, ksteps; uint32_t ph; bool some, first, last; } pv;  // the tile whose P V is to come
+            pv.some = false;
+            // Every group takes every fill of the rings in order, used or not: a phase's parity tells it from the ones
+            // beside it alone.
+            auto skip = [&]() {
+                const int st = (int)(n % NS);
+                if (!mbar_wait(full_bar(st), (n / NS) & 1u)) return false;
+                mbar_arrive(empty_bar(st));
+                ++n;
+                return true;
+            };
+            auto finish = [&]() {  // O (+)= P V
+                pv.some = false;
+                if (!mbar_wait(full_bar(pv.st), pv.ph) || !mbar_wait(prob_bar(w), probs & 1u)) return false;
+                ++probs;
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t qd = smem_desc_sw128(base + (q.slot & 1) * C::kTileBytes);
+                const uint64_t vd = pa_desc_v(base + C::kOffRing + pv.st * C::kTileBytes, C::kHalfBytes);
+                for (int k = 0; k < pv.ksteps; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
+                    tc_mma_f16_ts(oc, sc + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), !pv.first || k != 0);
+                tc_commit(empty_bar(pv.st));
+                if (pv.last) tc_commit(odone_bar(w));
+                return true;
+            };
+            while (ok) {
+                ok = mbar_wait(ifull_bar(ii), (ii / kPaItems) & 1u);
+                if (!ok || ring[ii % kPaItems].b < 0) break;
+                const PaItem& it = ring[ii % kPaItems];
+                const int t0 = it.t0, t1 = it.t1, end = it.end, nt0 = it.nt0, nq = it.nq;
+                const bool pair = it.nsub == 2;
+                const uint32_t slot = it.slot;
+                mbar_arrive(iempty_bar(ii));
+                ++ii;
+                // this group's tiles, and its Q tile (a single item's one is both groups')
+                const int from = pair ? t0 : t0 + w, to = pair && w == 0 ? nt0 : t1, step = pair ? 1 : 2;
+                const uint32_t own = slot + (nq == 2 ? w : 0);
+                for (int x = 0; ok && x < nq; ++x) {
+                    const uint32_t q = slot + x;
+                    ok = mbar_wait(qfull_bar((int)(q & 1)), (q >> 1) & 1u);
+                    if (ok && (q != own || from >= to)) mbar_arrive(qempty_bar((int)(q & 1)));
+                }
+                const uint64_t qd = smem_desc_sw128(base + (own & 1) * C::kTileBytes);
+                for (int t = t0; ok && t < t1; ++t) {
+                    if (pv.some && !(ok = finish())) break;
+                    if (t < from || t >= to || (t - from) % step != 0) {
+                        ok = skip() && skip();
+                        continue;
+                    }
+                    const int st = (int)(n % NS);
                     const uint64_t kd = smem_desc_sw128(base + C::kOffRing + st * C::kTileBytes);
+                    ok = mbar_wait(full_bar(st), (n / NS) & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {  // 16 dimensions (32 bytes) an instruction
                             const uint64_t o = (uint64_t)((h * C::kHalfBytes + k * 32) >> 4);
-                            tc_mma_f16_ss(tmem + 128u * q.w, qd + o, kd + o, kPaIdescQk, (h | k) != 0);
+                            tc_mma_f16_ss(sc, qd + o, kd + o, kPaIdescQk, (h | k) != 0);
                         }
-                    tc_commit(score_bar(q.w));
-                    if (q.frees) tc_commit(empty_bar(st));
-                    if (q.ends) {
-                        tc_commit(qempty_bar((int)(q.slot & 1)));
-                        if (q.nsub == 2) tc_commit(qempty_bar((int)((q.slot + 1) & 1)));
-                    }
+                    tc_commit(score_bar(w));
+                    tc_commit(empty_bar(st));
+                    pv.some = true;
+                    pv.st = (int)((n + 1) % NS);
+                    pv.ph = ((n + 1) / NS) & 1u;
+                    pv.ksteps = (min(kPaTile, end - t * kPaTile) + 15) / 16;
+                    pv.first = t == from;
+                    pv.last = t + step >= to;
+                    n += 2;
+                    if (pv.last) tc_commit(qempty_bar((int)(own & 1)));
                 }
-                __syncwarp();
-                busy |= 1u << q.w;
-                have = advance();
+                // the item's last P V: the group's next tile may be items away, and need the ring place this one holds
+                if (ok && pv.some) ok = finish();
             }
-            if (!ok) break;
-            if (behind.nsub == 0) {
-                if (behind.items == ahead.items) break;  // the last task is done
-                behind.load();
-            }
-            behind.next(p);
-            // O (+)= P V
-            const uint32_t vn = 2 * p.tile + 1;
-            const int st = (int)(vn % NS);
-            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (vn / NS) & 1u));
-            if (!ok) break;
-            const int ksteps = (p.valid + 15) / 16;
-            if (!I8 && p.fresh && p.valid % 16 != 0) {
-                // values behind the last position that anything sees: zeros (probability zero times whatever
-                // the page holds there would not be)
-                uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes;
-                for (int e = lane; e < (16 * ksteps - p.valid) * C::kHalves * 8; e += 32) {
-                    const int h = e / ((16 * ksteps - p.valid) * 8), r = p.valid + (e / 8) % (16 * ksteps - p.valid);
-                    *reinterpret_cast<uint4*>(vt + h * C::kHalfBytes + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            ok = __all_sync(0xffffffffu, mbar_wait(prob_bar(p.w), (probs >> p.w) & 1u));
-            if (!ok) break;
-            probs ^= 1u << p.w;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint64_t vd = pa_desc_v(base + C::kOffRing + st * C::kTileBytes, C::kHalfBytes);
-                for (int k = 0; k < ksteps; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
-                    tc_mma_f16_ts(tmem + 256u + 128u * p.w, tmem + 128u * p.w + 8u * k, vd + (uint64_t)(k * 2048 >> 4),
-                                  pa_idesc_pv<D>(), !p.first || k != 0);
-                if (p.frees) tc_commit(empty_bar(st));
-                if (p.last) tc_commit(odone_bar(p.w));
-            }
-            __syncwarp();
-            busy &= ~(1u << p.w);
-        }
-        // every MMA this thread issued has finished before TMEM is freed
-        if (lane == 0) {
-            tc_commit(drain_bar);
-            mbar_wait(drain_bar, 0);
+            // every MMA this thread issued has finished before TMEM is freed
+            tc_commit(drain_bar(w));
+            mbar_wait(drain_bar(w), 0);
         }
         __syncwarp();
     }
@@ -803,11 +724,15 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     if (!ok) break;
                     const uint8_t* src = sm + C::kOffRaw + rs * C::kRawBytes;
                     uint8_t* dst = sm + C::kOffRing + st * C::kTileBytes;
-#pragma unroll 4
-                    for (int e = th; e < kPaTile * D / 16; e += 128) {
-                        const int r = e / (D / 16), ch = e % (D / 16);  // row, run of 16 codes
-                        const uint4 w = *reinterpret_cast<const uint4*>(src + r * D + ch * 16);
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    constexpr int kRuns = D / 16, kPer = kPaTile * kRuns / 128;  // runs of 16 codes: of a row, of a thread
+                    uint4 w[kPer];
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x)
+                        w[x] = *reinterpret_cast<const uint4*>(src + (th + 128 * x) * 16);
+#pragma unroll
+                    for (int x = 0; x < kPer; ++x) {
+                        const int r = (th + 128 * x) / kRuns, ch = (th + 128 * x) % kRuns;
+                        const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
                         uint32_t o[8];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -849,19 +774,20 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         int4 began = make_int4(0, 0, 0, 0);
         while (const PaItem* item = take()) {
             const bool pair = item->nsub == 2;
-            const int t0 = item->t0, t1 = item->t1;
+            const int t0 = item->t0, t1 = item->t1, end = item->end;
             const int sub = pair ? w : 0;  // this group's sub-tile of the item
             const int tokens = min(a.tokens, item->tokens - sub * a.tokens);
             const bool live = tok < tokens;
             const bool warp_live = quad * 32 < tokens * a.group;
-            // positions that this row sees
-            const int vend = !live ? 0 : a.causal ? min(max(item->vend + sub * a.tokens + tok, 0), item->len) : item->len;
+            // positions that this row sees (a lane without a row is masked nowhere: its results go nowhere)
+            const int vend = !live ? kNoMask : a.causal ? min(max(item->vend + sub * a.tokens + tok, 0), item->len) : item->len;
             const int t_end = pair && w == 0 ? item->nt0 : t1;
             float m = -INFINITY, l = 0.0f;
             bool first = true;
             for (int t = t0; t < t1; ++t, ++tile) {
                 const bool mine = pair ? t < t_end : ((t - t0) & 1) == w;
                 const float* ks = nullptr;
+                const int valid = end - t * kPaTile;  // positions of the tile that some row sees
                 if constexpr (I8) {  // a tile of the other group's too: the ring's phases go by both
                     const int ss = (int)(tile % C::kSteps);
                     ok = __all_sync(0xffffffffu, mbar_wait(sfull_bar(ss), (tile / C::kSteps) & 1u));
@@ -906,7 +832,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
                     if (first) {
                         m = top;
-                    } else if (__any_sync(0xffffffffu, (top - m) * a.qscale > kPaMaxGrowth)) {
+                    } else if (__any_sync(0xffffffffu, live && (top - m) * a.qscale > kPaMaxGrowth)) {
                         const float mn = fmaxf(m, top);
                         const float alpha = m == mn ? 1.0f : ex2((m - mn) * a.qscale);
                         m = mn;
@@ -953,6 +879,19 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                         tmem_st16(ts + 16u * c, pk);
                     }
                     tmem_st_wait();
+                }
+                if (!I8 && mine && valid < kPaTile && valid % 16 != 0) {
+                    // values behind the last position that anything sees, in the last 16 that the product reads: zeros
+                    // (probability zero times whatever the page holds there would not be)
+                    const uint32_t n = 2 * tile + 1;
+                    const int st = (int)(n % NS);
+                    ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (n / NS) & 1u));
+                    if (!ok) break;
+                    const int rows = 16 - valid % 16;
+                    uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes + valid * 128;
+                    for (int e = quad * 32 + lane; e < rows * 8 * C::kHalves; e += 128)
+                        *reinterpret_cast<uint4*>(vt + e / (rows * 8) * C::kHalfBytes + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -65,6 +65,18 @@ def test_group_sizes(group, guard):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("H,Hkv,d", [(20, 5, 128), (8, 8, 64)])
+def test_many_items_of_mixed_lengths(H, Hkv, d, fmt, guard):
+    """More items than SMs: runs of one-tile sequences between long ones, so shares end anywhere and the softmax
+    groups' turns at the rings differ."""
+    rng = np.random.default_rng(H)
+    lens = [int(rng.choice([1, 60, 128, 129, 300, 700, 2500])) for _ in range(80)]
+    new = [int(min(L, rng.choice([1, 1, 1, 2, 20]))) for L in lens]
+    p = Paged(guard, new, lens, 64, Hkv, d, fmt, seed=H + 5)
+    run_attention(p, H, True, seed=H + 6)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
 def test_peaked_scores(fmt, guard):
     # large queries: the softmax is close to one-hot and the running maximum moves
     p = Paged(guard, [1, 64], [700, 300], 16, 5, 128, fmt, seed=77)

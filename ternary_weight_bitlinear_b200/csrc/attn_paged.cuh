@@ -60,6 +60,7 @@ struct PagedAttnArgs {
     int64_t q_stride, o_stride;
     int heads;
     int group;           // heads / kv_heads
+    FastDiv by_group;
     int tokens;          // tokens of a sub-tile: 128 / group
     int causal;
     int box;             // positions of a page box: the largest power of two up to 128 dividing page_size
@@ -125,14 +126,15 @@ struct PaWalk {
     int items;           // items per head of the sequence
     int slot = 0;        // Q tiles so far
 
-    __device__ __forceinline__ PaWalk(const PagedAttnArgs& args, const int64_t* plan) : a(args) {
+    __device__ __forceinline__ PaWalk(const PagedAttnArgs& args, const int64_t* plan, const KvSeq* seq) : a(args) {
         u0 = plan[0];
         u1 = plan[1];
         at = plan[2];
         b = (int)plan[3];
         g = (int)plan[4];
         i = (int)plan[5];
-        if (at < u1) load();
+        s = *seq;
+        items = pa_items(a, s.n);
     }
     __device__ __forceinline__ void load() {
         s = kv_seq(a.b, b);
@@ -180,15 +182,21 @@ struct PaWalk {
     }
 };
 
-// Units of one head of sequence b.
-__device__ __forceinline__ int64_t pa_seq_units(const PagedAttnArgs& a, int b) {
-    const KvSeq s = kv_seq(a.b, b);
-    const int items = pa_items(a, s.n);
-    int64_t u = 0;
-    for (int i = 0; i < items; ++i) {
+// How the items of a sequence are cut and what they cost (attn_rows.cuh has another way).
+struct PaCut {
+    static __device__ __forceinline__ int items(const PagedAttnArgs& a, int n) { return pa_items(a, n); }
+    static __device__ __forceinline__ int cost(const PagedAttnArgs& a, const KvSeq& s, int i) {
         int nsub, nt;
-        u += pa_cost(a, s, i, &nsub, &nt);
+        return pa_cost(a, s, i, &nsub, &nt);
     }
+};
+
+// Units of one head of a sequence.
+template <class Cut>
+__device__ __forceinline__ int64_t pa_seq_units(const PagedAttnArgs& a, const KvSeq& s) {
+    const int items = Cut::items(a, s.n);
+    int64_t u = 0;
+    for (int i = 0; i < items; ++i) u += Cut::cost(a, s, i);
     return u;
 }
 
@@ -212,54 +220,74 @@ __device__ __forceinline__ int64_t pa_scan(int64_t v, int64_t* warp_sums, int64_
     return v + before;
 }
 
+// This CTA's share of `total` units.
+__device__ __forceinline__ void pa_share(int64_t total, int64_t* u0, int64_t* u1) {
+    if (total < (1 << 22)) {  // 32-bit division (the grid has at most a few hundred CTAs)
+        *u0 = (uint32_t)total * blockIdx.x / gridDim.x;
+        *u1 = (uint32_t)total * (blockIdx.x + 1) / gridDim.x;
+    } else {
+        *u0 = total * blockIdx.x / gridDim.x;
+        *u1 = total * (blockIdx.x + 1) / gridDim.x;
+    }
+}
+
 // This CTA's share of all units, and the item that its first unit lies in:
-// plan = {u0, u1, first unit of that item, sequence, head, item}.  Every
-// thread of the CTA calls it; warp_sums has 16 words.
-__device__ __forceinline__ void pa_plan(const PagedAttnArgs& a, int64_t* plan, int64_t* warp_sums) {
+// plan = {u0, u1, first unit of that item, sequence, head, item, all units},
+// seq = that sequence.  Every thread of the CTA calls it; warp_sums has 16 words.
+constexpr int kPaPlanWords = 7;
+template <class Cut>
+__device__ __forceinline__ void pa_plan(const PagedAttnArgs& a, int64_t* plan, KvSeq* seq, int64_t* warp_sums) {
     const int nthr = blockDim.x;
     int64_t total = 0, mine = 0, upto = 0;
+    KvSeq s = {0, 0, 0};
+    auto units = [&](int b) {
+        if (b >= a.b.batch) return (int64_t)0;
+        s = kv_seq(a.b, b);
+        return pa_seq_units<Cut>(a, s) * a.c.kv_heads;
+    };
     for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
-        const int b = b0 + threadIdx.x;
-        mine = b < a.b.batch ? pa_seq_units(a, b) * a.c.kv_heads : 0;
+        mine = units(b0 + threadIdx.x);
         int64_t sum;
         upto = total + pa_scan(mine, warp_sums, &sum);
         total += sum;
     }
-    const int64_t u0 = total * blockIdx.x / gridDim.x, u1 = total * (blockIdx.x + 1) / gridDim.x;
+    int64_t u0, u1;
+    pa_share(total, &u0, &u1);
+    const bool once = a.b.batch <= nthr;  // else the sequences are passed over again
     if (threadIdx.x == 0) {
         plan[0] = u0;
         plan[1] = u1;
-        plan[2] = u1;  // nothing, unless found below
-        plan[3] = plan[4] = plan[5] = 0;
+        plan[6] = total;
+        if (u0 >= u1) plan[2] = u1;  // nothing
     }
-    __syncthreads();
-    if (u0 >= u1) return;
-    int64_t sum = 0;
-    for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
-        const int b = b0 + threadIdx.x;
-        if (a.b.batch > nthr) {  // several passes: scan again
-            mine = b < a.b.batch ? pa_seq_units(a, b) * a.c.kv_heads : 0;
-            int64_t s;
-            upto = sum + pa_scan(mine, warp_sums, &s);
-            sum += s;
-        }
-        if (mine > 0 && u0 >= upto - mine && u0 < upto) {
-            const int64_t per = mine / a.c.kv_heads, off = u0 - (upto - mine);
-            const int g = (int)(off / per);
-            int64_t at = upto - mine + g * per;
-            const KvSeq s = kv_seq(a.b, b);
-            int i = 0;
-            for (;;) {
-                int nsub, nt;
-                const int c = pa_cost(a, s, i, &nsub, &nt);
-                if (u0 < at + c) break;
-                at += c;
-                ++i;
+    if (u0 < u1) {
+        int64_t sum = 0;
+        for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
+            const int b = b0 + threadIdx.x;
+            if (!once) {
+                mine = units(b);
+                int64_t all;
+                upto = sum + pa_scan(mine, warp_sums, &all);
+                sum += all;
             }
-            plan[2] = at;
-            plan[3] = b;
-            plan[4] = g;
-            plan[5] = i;
+            if (mine > 0 && u0 >= upto - mine && u0 < upto) {
+                int64_t at = upto - mine;
+                const int64_t per = pa_seq_units<Cut>(a, s);
+                const int g = total < (1 << 22) ? (int)((uint32_t)(u0 - at) / (uint32_t)per) : (int)((u0 - at) / per);
+                at += g * per;
+                int i = 0;
+                for (;;) {
+                    const int c = Cut::cost(a, s, i);
+                    if (u0 < at + c) break;
+                    at += c;
+                    ++i;
+                }
+                plan[2] = at;
+                plan[3] = b;
+                plan[4] = g;
+                plan[5] = i;
+                *seq = s;
+            }
         }
     }
     __syncthreads();
@@ -408,7 +436,7 @@ __device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const 
         o[e] = 0.0f;
     }
     for (int j = j0; j < j1; ++j) {
-        const int page = kv_page(a.c, a.b, b, j), slot = j % a.c.page_size;
+        const int page = kv_page(a.c, a.b, b, j), slot = a.c.by_page.mod(j);
         if (page < 0) continue;
         const int64_t off = page * a.c.sp + slot * a.c.ss + g * a.c.sh + lane * DL;
         float x = 0.0f, v[DL];
@@ -461,9 +489,10 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     auto iempty_bar = [&](uint32_t i) { return item_bars + 8u * (kPaItems + i % kPaItems); };
     static_assert(kB2 + 14 + 2 * kPaItems == C::kBars, "barrier count");
     PaItem* ring = reinterpret_cast<PaItem*>(sm + C::kOffItems);
-    int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // 6 words
+    int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // kPaPlanWords
     int64_t* warp_sums = plan + 8;                                      // 16 words
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan + 24);
+    KvSeq* seq = reinterpret_cast<KvSeq*>(plan + 26);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -503,7 +532,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     // columns: scores (and probabilities) of group w at 128 w, output of group w at 256 + 128 w
     pdl_wait();
     pdl_launch_dependents();
-    pa_plan(a, plan, warp_sums);
+    pa_plan<PaCut>(a, plan, seq, warp_sums);
 
     bool ok = true;
     uint32_t ii = 0;  // items taken from the ring
@@ -524,7 +553,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     if (warp == 3) {
         // ---------------- scheduler, and the queries: one slot per sub-tile ----------------
         if (lane == 0) {
-            PaWalk walk(a, plan);
+            PaWalk walk(a, plan, seq);
             PaItem it;
             uint32_t n = 0, flying = 0;
             for (bool more = true; more && ok; ++ii) {
@@ -570,7 +599,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             int page = page_of(it.t0);
             for (int t = it.t0; t < it.t1; ++t, ++tile) {
                 const int page_next = page_of(t + 1);
-                const int slot0 = (t * kPaTile + lane * box) % a.c.page_size;
+                const int slot0 = a.c.by_page.mod(t * kPaTile + lane * box);
                 const int boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
                 if constexpr (I8) {
                     const int ss = (int)(tile % C::kSteps);
@@ -765,7 +794,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         setmaxnreg_inc<C::kRegsSoft>();
         const int w = (warp - 4) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
-        const int tok = row / a.group, hh = row % a.group;
+        const int tok = a.by_group.div(row), hh = a.by_group.mod(row);
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * w, to = tmem + lanes + 256u + 128u * w;
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);

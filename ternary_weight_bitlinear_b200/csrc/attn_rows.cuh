@@ -1,0 +1,748 @@
+// attn_rows.cuh -- attention over the paged cache for batches with few rows a
+// sequence and key/value head (decode steps, a few drafted tokens): the same
+// operation as attn_paged.cuh's, made for streaming the cache.
+//
+// With at most 16 rows against each position the products are far below what
+// the keys and values cost to read, so the kernel is built as a stream: a
+// position is read once for the (up to) 16 rows of its head, straight from its
+// page, and everything after the load stays in a warp's registers.
+//  * A loader warp moves chunks of 32 positions (keys, values, an int8 cache's
+//    steps) by TMA into stages; chunk n of the CTA goes to consumer warp
+//    n mod W, so a warp's stages are its own ring and no two warps wait for
+//    one another between items.
+//  * A consumer warp scores its chunk with mma.sync (m16n8k16, bf16: 16 rows
+//    are a quarter of the smallest tcgen05 tile's, which would also pass
+//    scores and probabilities through tensor memory), keeps the running
+//    maximum, sum and output of its positions, and feeds the probabilities of
+//    one product's result to the next as its operand without leaving
+//    registers.  int8 codes become bf16 (exactly) in registers, in the order
+//    in which shared memory gives them up in whole 16-byte words: the
+//    positions and dimensions of a product may stand in any order as long as
+//    both operands agree.
+//  * Items ((sequence, head, 16 rows) times their chunks) are shared out
+//    evenly over the CTAs as in attn_paged.cuh.  The warps of a CTA merge
+//    through shared memory; of the CTAs that hold parts of one item the last
+//    to arrive merges them, in the order of the CTAs (so the result does not
+//    depend on which it is).  One launch.
+#pragma once
+
+#include "attn_paged.cuh"
+
+namespace bl {
+
+constexpr int kRwRows = 16;       // rows of an item (MMA M)
+constexpr int kRwChunk = 32;      // positions of a chunk
+constexpr int kRwItemUnits = 4;   // cost of an item beside its chunks, in chunks
+constexpr int kRwItems = 4;       // ring of items
+
+template <int D, bool I8>
+struct RwCfg {
+    static constexpr int kWarps = D == 128 && !I8 ? 4 : 8;                    // consumer warps
+    static constexpr int kTileBytes = kRwChunk * D * (I8 ? 1 : 2);            // keys (or values) of a chunk
+    static constexpr int kStepBytes = I8 ? 2 * kRwChunk * 4 : 0;
+    static constexpr int kStageBytes = (2 * kTileBytes + kStepBytes + 1023) / 1024 * 1024;
+    static constexpr int kDepth = D == 128 ? (I8 ? 2 : 3) : (I8 ? 4 : 2);     // stages of a warp
+    static constexpr int kLoaders = 4;                                        // loader warps: chunk n is loader n mod kLoaders'
+    static constexpr int kThreads = 32 * (kWarps + kLoaders);
+    static constexpr int kOffO = kWarps * kDepth * kStageBytes;               // [warps][16][D] outputs
+    static constexpr int kOffMl = kOffO + kWarps * kRwRows * D * 4;           // [warps][16] (maximum, sum)
+    static constexpr int kOffItems = kOffMl + kWarps * kRwRows * 8;
+    static constexpr int kBars = 2 * kWarps * kDepth + 2 * kRwItems + 4;
+    static constexpr int kOffBar = kOffItems + kRwItems * 64;
+    static constexpr int kOffPlan = kOffBar + 8 * kBars;
+    static constexpr int kSmem = kOffPlan + 256 + 1024;  // plan words (28, of 8 bytes), alignment slack
+    static_assert(kSmem <= 227 * 1024, "shared memory budget");
+    static_assert((kWarps * kDepth) % kLoaders == 0, "a stage has one loader");
+};
+
+// An item and this CTA's part of it.
+struct RwItem {
+    int b, g;            // sequence, key/value head; b < 0: no more items
+    int q0;              // first row of the sequence in the batch
+    int row0, rows;      // rows of the item among the sequence's n * group of this head
+    int nt, t0, t1;      // its chunks, and this CTA's
+    int end;             // positions that some row of the item sees
+    int vbase, len;      // position of the sequence's first new token, positions of the sequence
+    int cta0, parts;     // first CTA with a part of the item, and how many have one
+    int spread;          // total < grid: a chunk a CTA, from unit (unit_hi, unit_lo) on
+    int unit_hi, unit_lo;
+};
+static_assert(sizeof(RwItem) == 64, "item words");
+
+__device__ __forceinline__ int rw_cost(const PagedAttnArgs& a, const KvSeq& s, int i, int* nt) {
+    const int last = min((i + 1) * kRwRows, s.n * a.group) - 1;  // the item's last row
+    *nt = (pa_end(a, s, a.by_group.div(last) + 1) + kRwChunk - 1) / kRwChunk;
+    return kRwItemUnits + *nt;
+}
+__device__ __forceinline__ int rw_items(const PagedAttnArgs& a, int n) {
+    return (n * a.group + kRwRows - 1) / kRwRows;
+}
+struct RwCut {
+    static __device__ __forceinline__ int items(const PagedAttnArgs& a, int n) { return rw_items(a, n); }
+    static __device__ __forceinline__ int cost(const PagedAttnArgs& a, const KvSeq& s, int i) {
+        int nt;
+        return rw_cost(a, s, i, &nt);
+    }
+};
+// The CTA whose share [total x / grid, total (x + 1) / grid) holds unit u.
+__device__ __forceinline__ int rw_cta_of(int64_t u, int64_t total) {
+    if (total < (1 << 22))  // 32-bit division (the grid has at most a few hundred CTAs)
+        return (int)((((uint32_t)u + 1) * gridDim.x + (uint32_t)total - 1) / (uint32_t)total) - 1;
+    return (int)(((u + 1) * gridDim.x + total - 1) / total) - 1;
+}
+
+struct RwWalk {
+    const PagedAttnArgs& a;
+    int64_t u0, u1, at, total;
+    int b, g, i, items;
+    KvSeq s;
+    __device__ __forceinline__ RwWalk(const PagedAttnArgs& args, const int64_t* plan, const KvSeq* seq) : a(args) {
+        u0 = plan[0];
+        u1 = plan[1];
+        at = plan[2];
+        b = (int)plan[3];
+        g = (int)plan[4];
+        i = (int)plan[5];
+        total = plan[6];
+        s = *seq;
+        items = rw_items(a, s.n);
+    }
+    __device__ __forceinline__ void load() {
+        s = kv_seq(a.b, b);
+        items = rw_items(a, s.n);
+    }
+    __device__ __forceinline__ bool next(RwItem& it) {
+        while (at < u1) {
+            int nt;
+            const int c = rw_cost(a, s, i, &nt);
+            const int64_t from = u0 - at - kRwItemUnits, to = u1 - at - kRwItemUnits;
+            const int lo = from > 0 ? (int)from : 0, hi = to >= nt ? nt : to > 0 ? (int)to : 0;
+            const bool mine = lo < hi || (nt == 0 && u0 <= at);
+            if (mine) {
+                it.b = b;
+                it.g = g;
+                it.q0 = s.q0;
+                it.row0 = i * kRwRows;
+                it.rows = min(kRwRows, s.n * a.group - it.row0);
+                it.nt = nt;
+                it.t0 = lo;
+                it.t1 = hi;
+                it.end = pa_end(a, s, a.by_group.div(it.row0 + it.rows - 1) + 1);
+                it.vbase = s.len - s.n;
+                it.len = s.len;
+                const int64_t first = at + kRwItemUnits;
+                it.spread = total < gridDim.x;
+                it.cta0 = it.parts = 0;
+                if (lo > 0 || hi < nt) {
+                    it.cta0 = rw_cta_of(first, total);
+                    it.parts = it.spread ? nt : rw_cta_of(at + c - 1, total) - it.cta0 + 1;
+                }
+                it.unit_hi = (int)(first >> 32);
+                it.unit_lo = (int)(first & 0xFFFFFFFF);
+            }
+            at += c;
+            if (++i == items) {
+                i = 0;
+                if (++g == a.c.kv_heads) {
+                    g = 0;
+                    while (++b < a.b.batch) {
+                        load();
+                        if (s.n > 0) break;
+                    }
+                    if (b >= a.b.batch) at = u1;
+                }
+            }
+            if (mine) return true;
+        }
+        return false;
+    }
+};
+
+__device__ __forceinline__ void st_release(unsigned long long* p, unsigned long long v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// Two codes (the low bytes of t's halves; the high ones may be anything) as
+// bf16: a code in two's complement is m - 128 s (m: low 7 bits, s: sign), and
+// (128 + m) - (128 + 128 s) has exact terms and an exact difference.
+__device__ __forceinline__ uint32_t codes2(uint32_t t) {
+    const uint32_t m = (t & 0x007F007Fu) | 0x43004300u, s = (t & 0x00800080u) | 0x43004300u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&s));
+    return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// The position that slot j of a product's eight stands for.  int8 rows of 128
+// bytes (in the 128-byte swizzle) are read 16 bytes a lane by slots 2k and
+// 2k + 1 together for the keys, and by the even or the odd slots together for
+// the values: rows 2k and 2k ^ 5 keep both free of bank conflicts.
+template <int D, bool I8>
+__device__ __forceinline__ int rw_slot(int j) {
+    if constexpr (I8 && D == 128) return (j & 1) ? (j - 1) ^ 5 : j;
+    return j;
+}
+// The dimension that column x of a merged output row stands for, and back
+// (int8: a lane reads D/8 neighbouring dimensions, one of each 8-column block).
+template <int D, bool I8>
+__device__ __forceinline__ int rw_column(int d) {
+    if constexpr (I8) return (d % (D / 8)) * 8 + d / (D / 8);
+    return d;
+}
+
+template <int D, bool I8>
+__global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+    const __grid_constant__ PagedAttnArgs a, unsigned long long* counters, unsigned long long epoch) {
+    using C = RwCfg<D, I8>;
+    constexpr int W = C::kWarps, NST = W * C::kDepth;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* sm = smem_raw + (base - raw);
+    const uint32_t bars = base + C::kOffBar;
+    auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bars + 8u * (NST + s); };
+    auto ifull_bar = [&](uint32_t i) { return bars + 8u * (2 * NST + i % kRwItems); };
+    auto iempty_bar = [&](uint32_t i) { return bars + 8u * (2 * NST + kRwItems + i % kRwItems); };
+    const uint32_t put_bar = bars + 8u * (2 * NST + 2 * kRwItems);      // the warps' results are in shared memory
+    const uint32_t got_bar = put_bar + 8u, sent_bar = put_bar + 16u, told_bar = put_bar + 24u;
+    RwItem* ring = reinterpret_cast<RwItem*>(sm + C::kOffItems);
+    int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // 7 words
+    int64_t* warp_sums = plan + 8;                                      // 16 words
+    KvSeq* seq = reinterpret_cast<KvSeq*>(plan + 26);
+    volatile int* last_flag = reinterpret_cast<volatile int*>(plan + 24);
+    unsigned* bad_rows = reinterpret_cast<unsigned*>(plan + 25);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int i = 0; i < kRwItems; ++i) {
+            mbar_init(ifull_bar(i), 1);
+            mbar_init(iempty_bar(i), W);
+        }
+        mbar_init(put_bar, W);
+        mbar_init(got_bar, W);
+        mbar_init(sent_bar, W);
+        mbar_init(told_bar, 1);
+        *bad_rows = 0;
+        mbar_init_fence();
+    }
+    if (warp == W && lane == 0) {
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    // this CTA's counter, for an item that begins here and goes on in others: this launch's, and nothing counted yet
+    if (threadIdx.x == 0) st_release(counters + blockIdx.x, epoch << 32);
+    pa_plan<RwCut>(a, plan, seq, warp_sums);
+
+    bool ok = true;
+    uint32_t ii = 0;
+    auto take = [&]() -> const RwItem* {
+        ok = __all_sync(0xffffffffu, mbar_wait(ifull_bar(ii), (ii / kRwItems) & 1u));
+        if (!ok) return nullptr;
+        const RwItem* it = ring + ii % kRwItems;
+        return it->b < 0 ? nullptr : it;
+    };
+    auto release = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(iempty_bar(ii));
+        ++ii;
+    };
+    if (warp >= W) {
+        // ---------------- the items (loader 0 hands them out), and their chunks ----------------
+        const int ld = warp - W;
+        const int box = min(a.box, kRwChunk), boxes = kRwChunk / box;
+        uint32_t n0 = 0, loaded = ld;  // chunks passed; this loader's next chunk
+        RwWalk walk(a, plan, seq);
+        RwItem it;
+        for (bool more = true; more; ++ii) {
+            more = walk.next(it);
+            if (!more) it.b = -1;
+            if (ld == 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(iempty_bar(ii), ((ii / kRwItems) & 1u) ^ 1u));
+                if (!ok) break;
+                if (lane == 0) {
+                    ring[ii % kRwItems] = it;
+                    mbar_arrive(ifull_bar(ii));
+                }
+                __syncwarp();
+            }
+            if (!more) break;
+            // the page table's next 32 entries, a lane each, and the 32 after them (on their way while the first are used)
+            const int32_t* table = a.b.pages + (int64_t)it.b * a.b.max_pages;
+            const int pages = a.c.by_page.div(it.end + a.c.page_size - 1);
+            auto entries = [&](int at) { return at + lane < pages ? __ldcg(table + at + lane) : -1; };
+            const int skip = (int)((ld + C::kLoaders - n0 % C::kLoaders) % C::kLoaders);
+            const uint32_t n = n0;  // the item's first chunk
+            n0 += it.t1 - it.t0;
+            int p0 = a.c.by_page.div((it.t0 + skip) * kRwChunk);
+            int now = entries(p0), next = entries(p0 + 32);
+            for (int t = it.t0 + skip; t < it.t1; t += C::kLoaders) {
+                // lane x: box x of the chunk (which spans at most two pages)
+                const int p = t * kRwChunk + lane * box;
+                const int at = a.c.by_page.div(p);
+                const int first = __shfl_sync(0xffffffffu, at, 0);
+                if (first + 1 >= p0 + 32) {  // the entries up to this chunk's are done with
+                    const int keep = first - p0;
+                    if (keep < 32) {
+                        const int x = __shfl_sync(0xffffffffu, now, (lane + keep) & 31), y = __shfl_sync(0xffffffffu, next, (lane + keep) & 31);
+                        now = lane + keep < 32 ? x : y;
+                    } else {
+                        now = entries(first);
+                    }
+                    p0 = first;
+                    next = entries(p0 + 32);
+                }
+                const int entry = __shfl_sync(0xffffffffu, now, (lane < boxes ? at - p0 : 0) & 31);
+                const int slot = p - at * a.c.page_size;
+                const bool wanted = lane < boxes && p < it.end, here = (unsigned)entry < (unsigned)a.c.num_pages;
+                if (wanted && !here) atomicOr(&g_status, kStatusBadPage);
+                const int page = wanted && here ? entry : -1;
+                const int some = __popc(__ballot_sync(0xffffffffu, page >= 0));
+                const uint32_t c = n + (t - it.t0), st = c % NST, fb = full_bar(st);
+                ok = __all_sync(0xffffffffu, mbar_wait(empty_bar(st), ((c / NST) & 1u) ^ 1u));
+                if (!ok) break;
+                loaded = c + C::kLoaders;
+                if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(some * box * (2 * D * (I8 ? 1 : 2) + (I8 ? 8 : 0))));
+                __syncwarp();
+                if (page >= 0) {
+                    const uint32_t kd = base + st * C::kStageBytes, vd = kd + C::kTileBytes;
+                    if constexpr (I8) {
+                        tma_load_4d(kd + lane * box * D, &map_k, 0, it.g, slot, page, fb);
+                        tma_load_4d(vd + lane * box * D, &map_v, 0, it.g, slot, page, fb);
+                        const int64_t off = ((int64_t)page * a.c.kv_heads + it.g) * a.c.page_size + slot;
+                        const uint32_t sd = vd + C::kTileBytes + lane * box * 4;
+                        bulk_g2s(sd, a.c.k_step + off, (uint32_t)box * 4, fb);
+                        bulk_g2s(sd + kRwChunk * 4, a.c.v_step + off, (uint32_t)box * 4, fb);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < D / 64; ++h) {
+                            tma_load_4d(kd + h * kRwChunk * 128 + lane * box * 128, &map_k, h * 64, it.g, slot, page, fb);
+                            tma_load_4d(vd + h * kRwChunk * 128 + lane * box * 128, &map_v, h * 64, it.g, slot, page, fb);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+        }
+        // after a failed wait, let this loader's copies still in flight land first (a stage has at most one)
+        if (!ok && lane == 0)
+            for (uint32_t j = 1; j <= NST / C::kLoaders; ++j) {
+                const uint32_t c = loaded - j * C::kLoaders;
+                if ((int)c >= 0) mbar_wait(full_bar(c % NST), (c / NST) & 1u);
+            }
+    } else {
+        // ---------------- consumers ----------------
+        const int w = warp, r8 = lane >> 2, kq = lane & 3;  // rows r8 and r8 + 8, quarter
+        float* osm = reinterpret_cast<float*>(sm + C::kOffO);
+        float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
+        bool begun = false;  // (thread 0) an item begins here and goes on in other CTAs: the last of them resets the counter
+        uint32_t n0 = 0, merges = 0, sent = 0, told = 0;  // chunks passed; phases of the barriers
+        while (const RwItem* item = take()) {
+            const int t0 = item->t0, t1 = item->t1, rows = item->rows, end = item->end;
+            const int64_t head0 = (int64_t)item->g * a.group;
+            // the queries of rows r8 and r8 + 8 as the products' A operand
+            uint32_t q[D / 16][4];
+            int vend[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int row = item->row0 + r8 + 8 * x, tok = a.by_group.div(row);
+                const bool live = r8 + 8 * x < rows;
+                vend[x] = !live ? 0 : a.causal ? min(max(item->vbase + tok + 1, 0), item->len) : item->len;
+                const uint16_t* src = a.q + (int64_t)(item->q0 + tok) * a.q_stride + (head0 + a.by_group.mod(row)) * D;
+                if constexpr (I8) {
+#pragma unroll
+                    for (int blk = 0; blk < D / 64; ++blk)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint4 v = live ? __ldcg(reinterpret_cast<const uint4*>(src + 64 * blk + 16 * kq + 8 * y))
+                                                 : make_uint4(0, 0, 0, 0);
+                            q[4 * blk + 2 * y][x] = v.x;
+                            q[4 * blk + 2 * y][x + 2] = v.y;
+                            q[4 * blk + 2 * y + 1][x] = v.z;
+                            q[4 * blk + 2 * y + 1][x + 2] = v.w;
+                        }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            q[k][x + 2 * y] = live ? __ldcg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 * y + 2 * kq)) : 0u;
+                }
+            }
+            const int vmin = a.causal ? item->vbase + a.by_group.div(item->row0) + 1 : item->len;  // of the item's first row
+            float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int db = 0; db < D / 8; ++db)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[db][c] = 0.0f;
+            const int skip = (int)((w + W - n0 % W) % W);
+            for (int t = t0 + skip; t < t1; t += W) {
+                const uint32_t n = n0 + (t - t0), st = n % NST;
+                ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (n / NST) & 1u));
+                if (!ok) break;
+                uint8_t* ktile = sm + st * C::kStageBytes;
+                uint8_t* vtile = ktile + C::kTileBytes;
+                const uint32_t ka = base + st * C::kStageBytes, va = ka + C::kTileBytes;
+                const float* steps = reinterpret_cast<const float*>(vtile + C::kTileBytes);
+                float s[4][4];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[nb][c] = 0.0f;
+                if constexpr (I8) {
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) {
+                        const int r = nb * 8 + rw_slot<D, I8>(r8);
+#pragma unroll
+                        for (int blk = 0; blk < D / 64; ++blk) {
+                            const int ch = D == 128 ? (4 * blk + kq) ^ (r & 7) : kq;
+                            const uint4 x = *reinterpret_cast<const uint4*>(ktile + r * D + ch * 16);
+                            const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                mma_bf16(s[nb], q[4 * blk + y], codes2(__byte_perm(ws[y], 0, 0x4140)),
+                                         codes2(__byte_perm(ws[y], 0, 0x4342)));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int p = 16 * i + (lane >> 4) * 8 + (lane & 7), ch = 2 * (k & 3) + ((lane >> 3) & 1);
+                            uint32_t bk[4];
+                            ldsm4(ka + (k >> 2) * kRwChunk * 128 + p * 128 + ((ch ^ (p & 7)) << 4), bk);
+                            mma_bf16(s[2 * i], q[k], bk[0], bk[1]);
+                            mma_bf16(s[2 * i + 1], q[k], bk[2], bk[3]);
+                        }
+                }
+                // scores in the log2 domain
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float f = a.qscale;
+                        if constexpr (I8) f *= steps[nb * 8 + rw_slot<D, I8>(2 * kq + (c & 1))];
+                        s[nb][c] *= f;
+                    }
+                const bool masked = t * kRwChunk + kRwChunk > vmin;
+                if (masked) {
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (t * kRwChunk + nb * 8 + rw_slot<D, I8>(2 * kq + (c & 1)) >= vend[c >> 1]) s[nb][c] = -INFINITY;
+                }
+                float top[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    top[x] = s[0][2 * x];
+#pragma unroll
+                    for (int nb = 0; nb < 4; ++nb) top[x] = fmaxf(top[x], fmaxf(s[nb][2 * x], s[nb][2 * x + 1]));
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+                }
+                if (__any_sync(0xffffffffu, top[0] - m[0] > kPaMaxGrowth || top[1] - m[1] > kPaMaxGrowth)) {
+                    float alpha[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float mn = fmaxf(m[x], top[x]);
+                        alpha[x] = m[x] == mn ? 1.0f : ex2(m[x] - mn);
+                        m[x] = mn;
+                        l[x] *= alpha[x];
+                    }
+#pragma unroll
+                    for (int db = 0; db < D / 8; ++db)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[db][c] *= alpha[c >> 1];
+                }
+                const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        s[nb][c] = ex2(s[nb][c] - ref[c >> 1]);
+                        l[c >> 1] += s[nb][c];
+                        if constexpr (I8) {
+                            const int p = nb * 8 + rw_slot<D, I8>(2 * kq + (c & 1));
+                            // (a step behind the last position may be anything)
+                            s[nb][c] = masked && t * kRwChunk + p >= vend[c >> 1] ? 0.0f : s[nb][c] * steps[kRwChunk + p];
+                        }
+                    }
+                if constexpr (!I8) {
+                    const int valid = end - t * kRwChunk;
+                    if (valid < kRwChunk) {
+                        // values behind the last position that anything sees: zeros (probability zero times whatever
+                        // the page holds there would not be)
+                        for (int e = lane; e < (kRwChunk - valid) * 8 * (D / 64); e += 32) {
+                            const int h = e / ((kRwChunk - valid) * 8), x = e % ((kRwChunk - valid) * 8);
+                            *reinterpret_cast<uint4*>(vtile + h * kRwChunk * 128 + valid * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        __syncwarp();
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t p[4] = {pack_bf16x2(s[2 * k][0], s[2 * k][1]), pack_bf16x2(s[2 * k][2], s[2 * k][3]),
+                                           pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]),
+                                           pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3])};
+                    if constexpr (I8) {
+                        constexpr int N = D / 32;  // words of a lane's run of D/8 dimensions
+                        uint32_t v[4][N];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {  // slots 2 kq and 2 kq + 1 of both eights
+                            const int r = (2 * k + (x >> 1)) * 8 + rw_slot<D, I8>(2 * kq + (x & 1));
+                            if constexpr (D == 128) {
+                                const uint4 y = *reinterpret_cast<const uint4*>(vtile + r * D + ((r8 ^ (r & 7)) << 4));
+                                v[x][0] = y.x;
+                                v[x][1] = y.y;
+                                v[x][2] = y.z;
+                                v[x][3] = y.w;
+                            } else {
+                                const uint2 y = *reinterpret_cast<const uint2*>(vtile + r * D + r8 * 8);
+                                v[x][0] = y.x;
+                                v[x][1] = y.y;
+                            }
+                        }
+#pragma unroll
+                        for (int db = 0; db < D / 8; ++db) {
+                            const uint32_t pick = (uint32_t)((db & 3) | ((4 + (db & 3)) << 8));  // its bytes 0 and 2
+                            mma_bf16(o[db], p, codes2(__byte_perm(v[0][db >> 2], v[1][db >> 2], pick)),
+                                     codes2(__byte_perm(v[2][db >> 2], v[3][db >> 2], pick)));
+                        }
+                    } else {
+#pragma unroll
+                        for (int db = 0; db < D / 8; db += 2) {
+                            const int r = 16 * k + ((lane >> 3) & 1) * 8 + (lane & 7), ch = (db & 7) + (lane >> 4);
+                            uint32_t bv[4];
+                            ldsm4t(va + (db >> 3) * kRwChunk * 128 + r * 128 + ((ch ^ (r & 7)) << 4), bv);
+                            mma_bf16(o[db], p, bv[0], bv[1]);
+                            mma_bf16(o[db + 1], p, bv[2], bv[3]);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty_bar(st));
+            }
+            if (!ok) break;
+            n0 += t1 - t0;
+            // ---- merge the CTA's warps ----
+            const bool whole = t0 == 0 && t1 == item->nt;
+            if (merges > 0) ok = __all_sync(0xffffffffu, mbar_wait(got_bar, (merges - 1) & 1u));  // the last item's are read
+            if (!ok) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+                const int r = r8 + 8 * x;
+                if (r < rows) {
+                    if (kq == 0) ml[w * kRwRows + r] = make_float2(m[x], l[x]);
+                    float* dst = osm + (w * kRwRows + r) * D + 2 * kq;
+                    if (t0 + skip < t1) {
+#pragma unroll
+                        for (int db = 0; db < D / 8; ++db)
+                            *reinterpret_cast<float2*>(dst + 8 * db) = make_float2(o[db][2 * x], o[db][2 * x + 1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(put_bar);
+            ok = __all_sync(0xffffffffu, mbar_wait(put_bar, merges & 1u));
+            if (!ok) break;
+            const int slot = t0 == 0 ? 1 : 0;
+            const int64_t prow = ((int64_t)blockIdx.x * 2 + slot) * kRwRows;
+            const int done0 = (int)((n0 - (t1 - t0)) % W);  // warp of the item's first chunk
+            const int used = min(t1 - t0, W);               // warps with chunks, from done0 on
+            for (int x = threadIdx.x; x < rows * (D / 2); x += 32 * W) {
+                const int r = x / (D / 2), d = x % (D / 2) * 2;
+                // the warps in the order of their first chunks
+                float2 v[W];
+                float mx = -INFINITY, den = 0.0f, n_0 = 0.0f, n_1 = 0.0f;
+#pragma unroll
+                for (int y = 0; y < W; ++y) {
+                    v[y] = y < used ? ml[(done0 + y) % W * kRwRows + r] : make_float2(-INFINITY, 0.0f);
+                    mx = fmaxf(mx, v[y].x);
+                }
+#pragma unroll
+                for (int y = 0; y < W; ++y) {
+                    const float f = v[y].x == -INFINITY ? 0.0f : ex2(v[y].x - mx);
+                    den = fmaf(f, v[y].y, den);
+                    if (y < used) {
+                        const float* src = osm + ((done0 + y) % W * kRwRows + r) * D;
+                        n_0 = fmaf(f, src[rw_column<D, I8>(d)], n_0);
+                        n_1 = fmaf(f, src[rw_column<D, I8>(d + 1)], n_1);
+                    }
+                }
+                if (!I8 && !(n_0 * 0.0f == 0.0f && n_1 * 0.0f == 0.0f)) atomicOr(bad_rows, 1u << r);
+                if (whole) {
+                    const int row = item->row0 + r, tok = a.by_group.div(row);
+                    const int ve = a.causal ? item->vbase + tok + 1 : item->len;
+                    *reinterpret_cast<uint32_t*>(a.out + (int64_t)(item->q0 + tok) * a.o_stride + (head0 + a.by_group.mod(row)) * D + d) =
+                        ve > 0 ? pack_bf16x2(n_0 / den, n_1 / den) : 0u;
+                } else {
+                    *reinterpret_cast<float2*>(a.part + (prow + r) * D + d) = make_float2(n_0, n_1);
+                    if (d == 0) *reinterpret_cast<float2*>(a.part_ml + (prow + r) * 2) = make_float2(mx, den);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(got_bar);
+            if constexpr (!I8) {
+                // an infinity or NaN came out: where it stands in a position that the row does not see, the row is
+                // computed from what it sees alone (as in attn_paged.cuh)
+                ok = __all_sync(0xffffffffu, mbar_wait(got_bar, merges & 1u));
+                if (!ok) break;
+                const unsigned bad = *reinterpret_cast<volatile unsigned*>(bad_rows);
+                for (int r = w; bad && r < rows; r += W) {
+                    if (!((bad >> r) & 1)) continue;
+                    const int row = item->row0 + r, tok = a.by_group.div(row);
+                    const int ve = a.causal ? min(max(item->vbase + tok + 1, 0), item->len) : item->len;
+                    const int64_t at = item->q0 + tok, head = head0 + a.by_group.mod(row);
+                    float x[D / 32], m2, l2;
+                    pa_row<D>(a, item->b, item->g, a.q + at * a.q_stride + head * D, t0 * kRwChunk,
+                              min(ve, t1 * kRwChunk), x, &m2, &l2);
+#pragma unroll
+                    for (int e = 0; e < D / 32; ++e) {
+                        const int d = lane * (D / 32) + e;
+                        if (whole)
+                            a.out[at * a.o_stride + head * D + d] = float_to_bf16_bits(ve > 0 ? x[e] / l2 : 0.0f);
+                        else
+                            a.part[(prow + r) * D + d] = x[e];
+                    }
+                    if (!whole && lane == 0) *reinterpret_cast<float2*>(a.part_ml + (prow + r) * 2) = make_float2(m2, l2);
+                }
+                if (bad) {  // cleared before the next item's results are looked at
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sent_bar);
+                    ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
+                    if (!ok) break;
+                    ++sent;
+                    if (threadIdx.x == 0) *bad_rows = 0;
+                }
+            }
+            ++merges;
+            if (!whole) {
+                // ---- the last CTA with a part of the item merges them ----
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sent_bar);
+                ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
+                if (!ok) break;
+                ++sent;
+                if (threadIdx.x == 0) {
+                    __threadfence();
+                    // once the CTA that the item begins in has set its counter for this launch (it was started
+                    // before this one, and set it first of all): chunks counted so far
+                    unsigned long long* ctr = counters + item->cta0;
+                    bool mine = false;
+                    for (int tries = 0; tries < (1 << 20) && !mine; ++tries) mine = ld_acquire(ctr) >> 32 == (epoch & 0xFFFFFFFFull);
+                    if (!mine) atomicOr(&g_status, kStatusTimeout);
+                    const unsigned chunks = (unsigned)(t1 - t0);
+                    const bool last = mine && (unsigned)(atomicAdd(ctr, (unsigned long long)chunks) & 0xFFFFFFFFull) + chunks == (unsigned)item->nt;
+                    // no count is left behind: a captured launch is replayed with its epoch
+                    if (last) st_release(ctr, 0);
+                    *last_flag = last;
+                    begun |= t0 == 0;
+                    mbar_arrive(told_bar);
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, mbar_wait(told_bar, told & 1u));
+                if (!ok) break;
+                ++told;
+                if (*last_flag) {
+                    __threadfence();
+                    const int parts = item->parts, cta0 = item->cta0;
+                    const int64_t unit0 = ((int64_t)item->unit_hi << 32) | (uint32_t)item->unit_lo;
+                    const int64_t total = plan[6];
+                    auto part_of = [&](int y) {  // row block of part y: slot 1 of the CTA the item begins in, slot 0 of the others
+                        const int x = item->spread ? rw_cta_of(unit0 + y, total) : cta0 + y;
+                        return ((int64_t)x * 2 + (y == 0 ? 1 : 0)) * kRwRows;
+                    };
+                    constexpr int DL = D / 32;
+                    for (int r = w; r < rows; r += W) {
+                        float mx = -INFINITY;
+                        for (int y = lane; y < parts; y += 32) mx = fmaxf(mx, __ldcg(a.part_ml + (part_of(y) + r) * 2));
+                        mx = warp_max_f(mx);
+                        float den = 0.0f, num[DL] = {};
+                        for (int y0 = 0; y0 < parts; y0 += 32) {
+                            float f = 0.0f, fl = 0.0f;
+                            int64_t from = 0;
+                            if (y0 + lane < parts) {
+                                from = part_of(y0 + lane) + r;
+                                const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + from * 2));
+                                f = v.x == -INFINITY ? 0.0f : ex2(v.x - mx);
+                                fl = f * v.y;
+                            }
+                            den += warp_sum_f(fl);
+                            const int count = min(32, parts - y0);
+                            for (int y = 0; y < count; y += 8) {  // 8 vectors on their way at once
+                                float v[8][DL];
+#pragma unroll
+                                for (int z = 0; z < 8; ++z) {
+                                    const float* src = a.part + __shfl_sync(0xffffffffu, from, y + z) * D + lane * DL;
+                                    if (y + z < count) {
+                                        if constexpr (DL == 4)
+                                            *reinterpret_cast<float4*>(v[z]) = __ldcg(reinterpret_cast<const float4*>(src));
+                                        else
+                                            *reinterpret_cast<float2*>(v[z]) = __ldcg(reinterpret_cast<const float2*>(src));
+                                    }
+                                }
+#pragma unroll
+                                for (int z = 0; z < 8; ++z) {
+                                    const float fz = __shfl_sync(0xffffffffu, f, y + z);
+                                    if (y + z < count) {
+#pragma unroll
+                                        for (int e = 0; e < DL; ++e) num[e] = fmaf(fz, v[z][e], num[e]);
+                                    }
+                                }
+                            }
+                        }
+                        const int row = item->row0 + r, tok = a.by_group.div(row);
+                        const int ve = a.causal ? item->vbase + tok + 1 : item->len;
+                        uint16_t* dst = a.out + (int64_t)(item->q0 + tok) * a.o_stride + (head0 + a.by_group.mod(row)) * D + lane * DL;
+#pragma unroll
+                        for (int e = 0; e < DL; e += 2)
+                            *reinterpret_cast<uint32_t*>(dst + e) = ve > 0 ? pack_bf16x2(num[e] / den, num[e + 1] / den) : 0u;
+                    }
+                }
+            }
+            release();
+        }
+        if (threadIdx.x == 0 && !begun) st_release(counters + blockIdx.x, 0);
+    }
+    __syncthreads();
+}
+
+}  // namespace bl

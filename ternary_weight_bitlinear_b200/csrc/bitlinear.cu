@@ -28,6 +28,7 @@
 #include "attn.cuh"
 #include "kvcache.cuh"
 #include "attn_paged.cuh"
+#include "attn_rows.cuh"
 
 namespace {
 
@@ -826,6 +827,8 @@ bl_status kv_check(const bl_kv_cache* c, const bl_kv_batch* b, int64_t T, KvCach
     ca->num_pages = (int)c->num_pages;
     ca->page_size = (int)c->page_size;
     ca->kv_heads = (int)c->kv_heads;
+    ca->by_page = fast_div(c->page_size);
+    ca->by_heads = fast_div(c->kv_heads);
     ba->cu_q = b->cu_q;
     ba->kv_len = b->kv_len;
     ba->pages = b->pages;
@@ -880,8 +883,9 @@ bool make_map_4d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes,
     return true;
 }
 
-// Layout of bitlinear_attn_paged's workspace: a description per CTA, then the
-// partial (max, sum) pairs and vectors of up to two cut items per CTA.
+// Layout of bitlinear_attn_paged's workspace: a description (or a counter) per
+// CTA, then the partial (max, sum) pairs and vectors of up to two cut items
+// per CTA.
 struct PagedWs {
     int64_t part_rows, desc_bytes, ml_bytes, bytes;
 };
@@ -889,10 +893,33 @@ PagedWs attn_paged_ws(int64_t T, int64_t group, int64_t head_dim, int sms) {
     const int64_t tokens = kPaRows / group;
     PagedWs w;
     w.part_rows = T <= tokens ? T * group : 2 * kPaRows;  // rows of an item: one sub-tile, or two
+    w.part_rows = std::max<int64_t>(w.part_rows, kRwRows);
     w.desc_bytes = ((int64_t)sms * 2 * sizeof(int4) + 255) / 256 * 256;
     w.ml_bytes = ((int64_t)sms * 2 * w.part_rows * 8 + 255) / 256 * 256;
     w.bytes = w.desc_bytes + w.ml_bytes + (int64_t)sms * 2 * w.part_rows * head_dim * 4;
     return w;
+}
+
+// Few rows against each position (attn_rows.cuh): 16 a sequence and key/value
+// head on average.  (The lengths themselves are on the device: either kernel
+// is right for every batch.)
+template <int D, bool I8>
+bl_status attn_rows_launch(PagedAttnArgs& a, int dev, const DeviceInfo& info, unsigned long long* counters,
+                           cudaStream_t stream) {
+    CUtensorMap map_k, map_v;
+    const int64_t kd[4] = {D, a.c.kv_heads, a.c.page_size, a.c.num_pages}, ks[3] = {a.c.sh, a.c.ss, a.c.sp};
+    const int kb[4] = {I8 ? D : 64, 1, std::min(a.box, kRwChunk), 1};
+    const CUtensorMapDataType kt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    const CUtensorMapSwizzle sw = I8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw) ||
+        !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw))
+        return BL_ERR_CUDA;
+    using C = RwCfg<D, I8>;
+    if (prepare_kernel(reinterpret_cast<const void*>(attn_rows_kernel<D, I8>), dev, info, C::kThreads, C::kSmem) < 0)
+        return BL_ERR_CUDA;
+    a.part_rows = kRwRows;
+    return launch(attn_rows_kernel<D, I8>, dim3((unsigned)info.sms), dim3(C::kThreads), (size_t)C::kSmem, stream, map_k,
+                  map_v, (const PagedAttnArgs&)a, counters, next_epoch());
 }
 
 template <int D, bool I8>
@@ -907,6 +934,8 @@ bl_status attn_paged_launch(PagedAttnArgs& a, void* workspace, int dev, const De
     a.tokens = kPaRows / a.group;
     a.box = kPaTile;
     while (a.c.page_size % a.box != 0) a.box /= 2;
+    if ((int64_t)a.b.T * a.group <= (int64_t)kRwRows * a.b.batch)
+        return attn_rows_launch<D, I8>(a, dev, info, reinterpret_cast<unsigned long long*>(ws), stream);
     CUtensorMap map_q, map_k, map_v;
     const int64_t qd[4] = {D, a.group, a.b.T, a.c.kv_heads}, qs[3] = {D, a.q_stride, (int64_t)a.group * D};
     const int qb[4] = {64, a.group, a.tokens, 1};
@@ -1444,6 +1473,7 @@ bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batc
     a.o_stride = out_stride;
     a.heads = (int)q_heads;
     a.group = (int)(q_heads / cache->kv_heads);
+    a.by_group = fast_div(a.group);
     a.causal = causal != 0;
     a.qscale = scale * kLog2e;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

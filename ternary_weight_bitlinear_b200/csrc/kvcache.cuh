@@ -28,6 +28,22 @@ namespace bl {
 constexpr int kKvThreads = 128;
 constexpr int64_t kKvMaxPositions = 1 << 30;  // of a page table's row: position arithmetic stays in 32 bits
 
+// Division of x < 2^31 by a divisor known on the host: with s = ceil(log2 d)
+// and m = ceil(2^(31 + s) / d), m d exceeds 2^(31 + s) by less than d <= 2^s,
+// so x m / 2^(31 + s) exceeds x / d by less than 1 / d and floors the same.
+struct FastDiv {
+    uint32_t d, m;
+    int s;
+    __device__ __forceinline__ int div(int x) const { return d == 1 ? x : (int)(__umulhi((uint32_t)x, m) >> (s - 1)); }
+    __device__ __forceinline__ int mod(int x) const { return x - div(x) * (int)d; }
+};
+inline FastDiv fast_div(int64_t d) {
+    FastDiv f = {(uint32_t)d, 0, 0};
+    while (((int64_t)1 << f.s) < d) ++f.s;
+    f.m = (uint32_t)((((uint64_t)1 << (31 + f.s)) + d - 1) / d);
+    return f;
+}
+
 struct KvCacheArgs {
     void* k;                     // bf16 or int8 pages
     void* v;
@@ -35,6 +51,7 @@ struct KvCacheArgs {
     float* v_step;
     int64_t sp, ss, sh;          // strides in elements: page, slot, head
     int num_pages, page_size, kv_heads;
+    FastDiv by_page, by_heads;
 };
 
 struct KvBatchArgs {
@@ -78,7 +95,7 @@ __device__ __forceinline__ int kv_seq_of_row(const KvBatchArgs& a, int t, int la
 // Page of position p of sequence b, or -1 (recorded in the status word) when
 // the table's entry is not a page of the cache.
 __device__ __forceinline__ int kv_page(const KvCacheArgs& c, const KvBatchArgs& a, int b, int p) {
-    const int page = __ldcg(a.pages + (int64_t)b * a.max_pages + p / c.page_size);
+    const int page = __ldcg(a.pages + (int64_t)b * a.max_pages + c.by_page.div(p));
     if ((unsigned)page < (unsigned)c.num_pages) return page;
     atomicOr(&g_status, kStatusBadPage);
     return -1;
@@ -95,7 +112,7 @@ __device__ __forceinline__ bool kv_place(const KvCacheArgs& c, const KvBatchArgs
     if (t < s.q0 || pos < 0) return false;
     const int page = kv_page(c, a, b, pos);
     if (page < 0) return false;
-    const int slot = pos % c.page_size;
+    const int slot = c.by_page.mod(pos);
     *off = page * c.sp + slot * c.ss + head * c.sh;
     *step_off = ((int64_t)page * c.kv_heads + head) * c.page_size + slot;
     return true;

@@ -77,6 +77,17 @@ def test_many_items_of_mixed_lengths(H, Hkv, d, fmt, guard):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("H,Hkv,d", [(20, 5, 128), (8, 8, 64), (16, 2, 128)])
+def test_many_decode_rows_and_one_chunk(H, Hkv, d, fmt, guard):
+    """Decode rows (few rows a sequence on average) with one sequence of many rows among them."""
+    rng = np.random.default_rng(H + 1)
+    lens = [int(rng.choice([1, 31, 32, 33, 300, 1900])) for _ in range(60)] + [333]
+    new = [1] * 30 + [2, 0] * 15 + [50]
+    p = Paged(guard, [min(a, b) for a, b in zip(new, lens)], lens, 16, Hkv, d, fmt, seed=H + 7, pad=3)
+    run_attention(p, H, True, seed=H + 8)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
 def test_peaked_scores(fmt, guard):
     # large queries: the softmax is close to one-hot and the running maximum moves
     p = Paged(guard, [1, 64], [700, 300], 16, 5, 128, fmt, seed=77)

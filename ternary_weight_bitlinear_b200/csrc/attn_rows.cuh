@@ -43,6 +43,9 @@ struct RwCfg {
     static constexpr int kStageBytes = (2 * kTileBytes + kStepBytes + 1023) / 1024 * 1024;
     static constexpr int kDepth = D == 128 ? (I8 ? 2 : 3) : (I8 ? 4 : 2);     // stages of a warp
     static constexpr int kLoaders = 4;                                        // loader warps: chunk n is loader n mod kLoaders'
+    // registers a thread: with eight consumer warps the loaders hand theirs over (a warpgroup each way)
+    static constexpr int kRegsLoad = 72, kRegsUse = 216;
+    static_assert(kWarps == 4 || kRegsLoad + 2 * kRegsUse <= 3 * 168, "register shares");
     static constexpr int kThreads = 32 * (kWarps + kLoaders);
     static constexpr int kOffO = kWarps * kDepth * kStageBytes;               // [warps][16][D] outputs
     static constexpr int kOffMl = kOffO + kWarps * kRwRows * D * 4;           // [warps][16] (maximum, sum)
@@ -171,7 +174,7 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
         *bad_rows = 0;
         mbar_init_fence();
     }
-    if (warp == W && lane == 0) {
+    if (warp == 0 && lane == 0) {
         prefetch_map(&map_k);
         prefetch_map(&map_v);
     }
@@ -278,9 +281,10 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
         if (lane == 0) mbar_arrive(iempty_bar(ii));
         ++ii;
     };
-    if (warp >= W) {
+    if (warp < C::kLoaders) {
+        if constexpr (W == 8) setmaxnreg_dec<C::kRegsLoad>();
         // ---------------- the items (loader 0 hands them out), and their chunks ----------------
-        const int ld = warp - W;
+        const int ld = warp;
         const int box = min(a.box, kRwChunk), boxes = kRwChunk / box;
         uint32_t n0 = 0, loaded = ld;  // chunks passed; this loader's next chunk
         RwWalk walk(a, plan, seq);
@@ -364,10 +368,12 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
             }
     } else {
         // ---------------- consumers ----------------
-        const int w = warp, r8 = lane >> 2, kq = lane & 3;  // rows r8 and r8 + 8, quarter
+        if constexpr (W == 8) setmaxnreg_inc<C::kRegsUse>();
+        const int ct = threadIdx.x - 32 * C::kLoaders;  // thread among the consumers
+        const int w = ct >> 5, r8 = lane >> 2, kq = lane & 3;  // rows r8 and r8 + 8, quarter
         float* osm = reinterpret_cast<float*>(sm + C::kOffO);
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
-        bool begun = false;  // (thread 0) an item begins here and goes on in other CTAs: the last of them resets the counter
+        bool begun = false;  // (consumer 0) an item begins here and goes on in other CTAs: the last of them resets the counter
         uint32_t n0 = 0, merges = 0, sent = 0, told = 0;  // chunks passed; phases of the barriers
         while (const RwItem* item = take()) {
             const int t0 = item->t0, t1 = item->t1, rows = item->rows, end = item->end;
@@ -423,18 +429,21 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                     for (int c = 0; c < 4; ++c) s[nb][c] = 0.0f;
                 if constexpr (I8) {
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) {
-                        const int r = nb * 8 + rw_slot<D, I8>(r8);
+                    for (int blk = 0; blk < D / 64; ++blk) {
+                        uint4 x[4];
 #pragma unroll
-                        for (int blk = 0; blk < D / 64; ++blk) {
-                            const int ch = D == 128 ? (4 * blk + kq) ^ (r & 7) : kq;
-                            const uint4 x = *reinterpret_cast<const uint4*>(ktile + r * D + ch * 16);
-                            const uint32_t ws[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                mma_bf16(s[nb], q[4 * blk + y], codes2(__byte_perm(ws[y], 0, 0x4140)),
-                                         codes2(__byte_perm(ws[y], 0, 0x4342)));
+                        for (int nb = 0; nb < 4; ++nb) {
+                            const int r = nb * 8 + rw_slot<D, I8>(r8);
+                            x[nb] = *reinterpret_cast<const uint4*>(ktile + r * D + (D == 128 ? (4 * blk + kq) ^ (r & 7) : kq) * 16);
                         }
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+#pragma unroll
+                            for (int nb = 0; nb < 4; ++nb) {  // four sums in turn: a product waits for the one before it in its own
+                                const uint32_t word = y == 0 ? x[nb].x : y == 1 ? x[nb].y : y == 2 ? x[nb].z : x[nb].w;
+                                mma_bf16(s[nb], q[4 * blk + y], codes2(__byte_perm(word, 0, 0x4140)),
+                                         codes2(__byte_perm(word, 0, 0x4342)));
+                            }
                     }
                 } else {
 #pragma unroll
@@ -586,7 +595,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
             const int64_t prow = ((int64_t)blockIdx.x * 2 + slot) * kRwRows;
             const int done0 = (int)((n0 - (t1 - t0)) % W);  // warp of the item's first chunk
             const int used = min(t1 - t0, W);               // warps with chunks, from done0 on
-            for (int x = threadIdx.x; x < rows * (D / 2); x += 32 * W) {
+            for (int x = ct; x < rows * (D / 2); x += 32 * W) {
                 const int r = x / (D / 2), d = x % (D / 2) * 2;
                 // the warps in the order of their first chunks
                 float2 v[W];
@@ -649,7 +658,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                     ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
                     if (!ok) break;
                     ++sent;
-                    if (threadIdx.x == 0) *bad_rows = 0;
+                    if (ct == 0) *bad_rows = 0;
                 }
             }
             ++merges;
@@ -661,7 +670,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                 ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
                 if (!ok) break;
                 ++sent;
-                if (threadIdx.x == 0) {
+                if (ct == 0) {
                     __threadfence();
                     // once the CTA that the item begins in has set its counter for this launch (it was started
                     // before this one, and set it first of all): chunks counted so far
@@ -740,7 +749,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
             }
             release();
         }
-        if (threadIdx.x == 0 && !begun) st_release(counters + blockIdx.x, 0);
+        if (ct == 0 && !begun) st_release(counters + blockIdx.x, 0);
     }
     __syncthreads();
 }

@@ -10,12 +10,12 @@
 //    steps) by TMA into stages; chunk n of the CTA goes to consumer warp
 //    n mod W, so a warp's stages are its own ring and no two warps wait for
 //    one another between items.
-//  * A consumer warp scores its chunk with mma.sync (m16n8k16, bf16: 16 rows
-//    are a quarter of the smallest tcgen05 tile's, which would also pass
-//    scores and probabilities through tensor memory), keeps the running
-//    maximum, sum and output of its positions, and feeds the probabilities of
-//    one product's result to the next as its operand without leaving
-//    registers.  int8 codes become bf16 (exactly) in registers, in the order
+//  * A consumer warp scores its chunk with mma.sync (m16n8k16, bf16: the
+//    positions are its 16 rows and the item's rows its 8 columns, where a
+//    tcgen05 tile has 64 rows at least and would also pass scores and
+//    probabilities through tensor memory), keeps the running maximum, sum and
+//    output of its positions, and feeds the probabilities of one product to the
+//    next without leaving registers.  int8 codes become bf16 (exactly) in registers, in the order
 //    in which shared memory gives them up in whole 16-byte words: the
 //    positions and dimensions of a product may stand in any order as long as
 //    both operands agree.
@@ -30,12 +30,13 @@
 
 namespace bl {
 
-constexpr int kRwRows = 16;       // rows of an item (MMA M)
+constexpr int kRwRows = 16;       // most rows of an item
 constexpr int kRwChunk = 32;      // positions of a chunk
 constexpr int kRwItemUnits = 4;   // cost of an item beside its chunks, in chunks
 constexpr int kRwItems = 4;       // ring of items
 
-template <int D, bool I8>
+// NR: rows of an item, 8 or 16.
+template <int D, bool I8, int NR>
 struct RwCfg {
     static constexpr int kWarps = D == 128 && !I8 ? 4 : 8;                    // consumer warps
     static constexpr int kTileBytes = kRwChunk * D * (I8 ? 1 : 2);            // keys (or values) of a chunk
@@ -47,9 +48,11 @@ struct RwCfg {
     static constexpr int kRegsLoad = 72, kRegsUse = 216;
     static_assert(kWarps == 4 || kRegsLoad + 2 * kRegsUse <= 3 * 168, "register shares");
     static constexpr int kThreads = 32 * (kWarps + kLoaders);
-    static constexpr int kOffO = kWarps * kDepth * kStageBytes;               // [warps][16][D] outputs
-    static constexpr int kOffMl = kOffO + kWarps * kRwRows * D * 4;           // [warps][16] (maximum, sum)
-    static constexpr int kOffItems = kOffMl + kWarps * kRwRows * 8;
+    // floats of a merged row: four more than D keep its stores free of bank conflicts (16 rows of 128 bf16 have no room)
+    static constexpr int kOStride = D == 128 && !I8 && NR == 16 ? D : D + 4;
+    static constexpr int kOffO = kWarps * kDepth * kStageBytes;               // [warps][NR][kOStride] outputs
+    static constexpr int kOffMl = kOffO + kWarps * NR * kOStride * 4;         // [warps][NR] (maximum, sum)
+    static constexpr int kOffItems = kOffMl + kWarps * NR * 8;
     static constexpr int kBars = 2 * kWarps * kDepth + 2 * kRwItems + 4;
     static constexpr int kOffBar = kOffItems + kRwItems * 64;
     static constexpr int kOffPlan = kOffBar + 8 * kBars;
@@ -72,19 +75,22 @@ struct RwItem {
 };
 static_assert(sizeof(RwItem) == 64, "item words");
 
+template <int NR>
 __device__ __forceinline__ int rw_cost(const PagedAttnArgs& a, const KvSeq& s, int i, int* nt) {
-    const int last = min((i + 1) * kRwRows, s.n * a.group) - 1;  // the item's last row
+    const int last = min((i + 1) * NR, s.n * a.group) - 1;  // the item's last row
     *nt = (pa_end(a, s, a.by_group.div(last) + 1) + kRwChunk - 1) / kRwChunk;
     return kRwItemUnits + *nt;
 }
+template <int NR>
 __device__ __forceinline__ int rw_items(const PagedAttnArgs& a, int n) {
-    return (n * a.group + kRwRows - 1) / kRwRows;
+    return (n * a.group + NR - 1) / NR;
 }
+template <int NR>
 struct RwCut {
-    static __device__ __forceinline__ int items(const PagedAttnArgs& a, int n) { return rw_items(a, n); }
+    static __device__ __forceinline__ int items(const PagedAttnArgs& a, int n) { return rw_items<NR>(a, n); }
     static __device__ __forceinline__ int cost(const PagedAttnArgs& a, const KvSeq& s, int i) {
         int nt;
-        return rw_cost(a, s, i, &nt);
+        return rw_cost<NR>(a, s, i, &nt);
     }
 };
 // The CTA whose share [total x / grid, total (x + 1) / grid) holds unit u.
@@ -94,6 +100,7 @@ __device__ __forceinline__ int rw_cta_of(int64_t u, int64_t total) {
     return (int)(((u + 1) * gridDim.x + total - 1) / total) - 1;
 }
 
+template <int NR>
 struct RwWalk {
     const PagedAttnArgs& a;
     int64_t u0, u1, at, total;
@@ -108,16 +115,16 @@ struct RwWalk {
         i = (int)plan[5];
         total = plan[6];
         s = *seq;
-        items = rw_items(a, s.n);
+        items = rw_items<NR>(a, s.n);
     }
     __device__ __forceinline__ void load() {
         s = kv_seq(a.b, b);
-        items = rw_items(a, s.n);
+        items = rw_items<NR>(a, s.n);
     }
     __device__ __forceinline__ bool next(RwItem& it) {
         while (at < u1) {
             int nt;
-            const int c = rw_cost(a, s, i, &nt);
+            const int c = rw_cost<NR>(a, s, i, &nt);
             const int64_t from = u0 - at - kRwItemUnits, to = u1 - at - kRwItemUnits;
             const int lo = from > 0 ? (int)from : 0, hi = to >= nt ? nt : to > 0 ? (int)to : 0;
             const bool mine = lo < hi || (nt == 0 && u0 <= at);
@@ -125,8 +132,8 @@ struct RwWalk {
                 it.b = b;
                 it.g = g;
                 it.q0 = s.q0;
-                it.row0 = i * kRwRows;
-                it.rows = min(kRwRows, s.n * a.group - it.row0);
+                it.row0 = i * NR;
+                it.rows = min(NR, s.n * a.group - it.row0);
                 it.nt = nt;
                 it.t0 = lo;
                 it.t1 = hi;
@@ -180,6 +187,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// An 8 x 8 matrix of 16-bit values transposed across the warp.
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -216,11 +229,11 @@ __device__ __forceinline__ int rw_column(int d) {
     return d;
 }
 
-template <int D, bool I8>
-__global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
+template <int D, bool I8, int NR>
+__global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
     const __grid_constant__ PagedAttnArgs a, unsigned long long* counters, unsigned long long epoch) {
-    using C = RwCfg<D, I8>;
+    using C = RwCfg<D, I8, NR>;
     constexpr int W = C::kWarps, NST = W * C::kDepth;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -266,7 +279,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
     pdl_launch_dependents();
     // this CTA's counter, for an item that begins here and goes on in others: this launch's, and nothing counted yet
     if (threadIdx.x == 0) st_release(counters + blockIdx.x, epoch << 32);
-    pa_plan<RwCut>(a, plan, seq, warp_sums);
+    pa_plan<RwCut<NR>>(a, plan, seq, warp_sums);
 
     bool ok = true;
     uint32_t ii = 0;
@@ -287,7 +300,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
         const int ld = warp;
         const int box = min(a.box, kRwChunk), boxes = kRwChunk / box;
         uint32_t n0 = 0, loaded = ld;  // chunks passed; this loader's next chunk
-        RwWalk walk(a, plan, seq);
+        RwWalk<NR> walk(a, plan, seq);
         RwItem it;
         for (bool more = true; more; ++ii) {
             more = walk.next(it);
@@ -370,7 +383,12 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
         // ---------------- consumers ----------------
         if constexpr (W == 8) setmaxnreg_inc<C::kRegsUse>();
         const int ct = threadIdx.x - 32 * C::kLoaders;  // thread among the consumers
-        const int w = ct >> 5, r8 = lane >> 2, kq = lane & 3;  // rows r8 and r8 + 8, quarter
+        // The products have the positions (or dimensions) as their 16-row side and the item's rows as columns of eight:
+        //   S^T = K Q^T,  O^T = V^T P^T,
+        // so eight rows are a whole product.  In a result this lane holds rows 8 x + 2 kq and 8 x + 2 kq + 1 at position
+        // (dimension) slots r8 and r8 + 8.
+        constexpr int X = NR / 8;
+        const int w = ct >> 5, r8 = lane >> 2, kq = lane & 3;
         float* osm = reinterpret_cast<float*>(sm + C::kOffO);
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
         bool begun = false;  // (consumer 0) an item begins here and goes on in other CTAs: the last of them resets the counter
@@ -378,14 +396,13 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
         while (const RwItem* item = take()) {
             const int t0 = item->t0, t1 = item->t1, rows = item->rows, end = item->end;
             const int64_t head0 = (int64_t)item->g * a.group;
-            // the queries of rows r8 and r8 + 8 as the products' A operand
-            uint32_t q[D / 16][4];
-            int vend[2];
+            // the queries of rows 8 x + r8 as the products' B operand
+            uint32_t q[D / 16][X][2];
+            int vend[X][2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int row = item->row0 + r8 + 8 * x, tok = a.by_group.div(row);
-                const bool live = r8 + 8 * x < rows;
-                vend[x] = !live ? 0 : a.causal ? min(max(item->vbase + tok + 1, 0), item->len) : item->len;
+            for (int x = 0; x < X; ++x) {
+                const int row = item->row0 + 8 * x + r8, tok = a.by_group.div(row);
+                const bool live = 8 * x + r8 < rows;
                 const uint16_t* src = a.q + (int64_t)(item->q0 + tok) * a.q_stride + (head0 + a.by_group.mod(row)) * D;
                 if constexpr (I8) {
 #pragma unroll
@@ -394,25 +411,35 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                         for (int y = 0; y < 2; ++y) {
                             const uint4 v = live ? __ldcg(reinterpret_cast<const uint4*>(src + 64 * blk + 16 * kq + 8 * y))
                                                  : make_uint4(0, 0, 0, 0);
-                            q[4 * blk + 2 * y][x] = v.x;
-                            q[4 * blk + 2 * y][x + 2] = v.y;
-                            q[4 * blk + 2 * y + 1][x] = v.z;
-                            q[4 * blk + 2 * y + 1][x + 2] = v.w;
+                            q[4 * blk + 2 * y][x][0] = v.x;
+                            q[4 * blk + 2 * y][x][1] = v.y;
+                            q[4 * blk + 2 * y + 1][x][0] = v.z;
+                            q[4 * blk + 2 * y + 1][x][1] = v.w;
                         }
                 } else {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                         for (int y = 0; y < 2; ++y)
-                            q[k][x + 2 * y] = live ? __ldcg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 * y + 2 * kq)) : 0u;
+                            q[k][x][y] = live ? __ldcg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 * y + 2 * kq)) : 0u;
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {  // positions that rows 8 x + 2 kq + j see
+                    const int r = 8 * x + 2 * kq + j, tk = a.by_group.div(item->row0 + r);
+                    vend[x][j] = r >= rows ? 0 : a.causal ? min(max(item->vbase + tk + 1, 0), item->len) : item->len;
                 }
             }
             const int vmin = a.causal ? item->vbase + a.by_group.div(item->row0) + 1 : item->len;  // of the item's first row
-            float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            float o[D / 16][X][4], m[X][2], l[X][2];
 #pragma unroll
-            for (int db = 0; db < D / 8; ++db)
+            for (int x = 0; x < X; ++x) {
+                m[x][0] = m[x][1] = -INFINITY;
+                l[x][0] = l[x][1] = 0.0f;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) o[db][c] = 0.0f;
+                for (int db = 0; db < D / 16; ++db)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) o[db][x][c] = 0.0f;
+            }
             const int skip = (int)((w + W - n0 % W) % W);
             for (int t = t0 + skip; t < t1; t += W) {
                 const uint32_t n = n0 + (t - t0), st = n % NST;
@@ -421,144 +448,169 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                 uint8_t* ktile = sm + st * C::kStageBytes;
                 uint8_t* vtile = ktile + C::kTileBytes;
                 const uint32_t ka = base + st * C::kStageBytes, va = ka + C::kTileBytes;
-                const float* steps = reinterpret_cast<const float*>(vtile + C::kTileBytes);
-                float s[4][4];
+                float ks[2][2], vs[2][2];  // steps of this lane's four positions
+                if constexpr (I8) {
+                    const float* steps = reinterpret_cast<const float*>(vtile + C::kTileBytes) + rw_slot<D, I8>(r8);
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb)
+                    for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) s[nb][c] = 0.0f;
+                        for (int h = 0; h < 2; ++h) {
+                            ks[pb][h] = steps[16 * pb + 8 * h] * a.qscale;
+                            vs[pb][h] = steps[kRwChunk + 16 * pb + 8 * h];
+                        }
+                }
+                float s[2][X][4];
+#pragma unroll
+                for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+                    for (int x = 0; x < X; ++x)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[pb][x][c] = 0.0f;
                 if constexpr (I8) {
 #pragma unroll
                     for (int blk = 0; blk < D / 64; ++blk) {
-                        uint4 x[4];
+                        uint4 y[4];  // 16 codes of the four positions
 #pragma unroll
                         for (int nb = 0; nb < 4; ++nb) {
                             const int r = nb * 8 + rw_slot<D, I8>(r8);
-                            x[nb] = *reinterpret_cast<const uint4*>(ktile + r * D + (D == 128 ? (4 * blk + kq) ^ (r & 7) : kq) * 16);
+                            y[nb] = *reinterpret_cast<const uint4*>(ktile + r * D + (D == 128 ? (4 * blk + kq) ^ (r & 7) : kq) * 16);
                         }
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
+                        for (int k = 0; k < 4; ++k)
 #pragma unroll
-                            for (int nb = 0; nb < 4; ++nb) {  // four sums in turn: a product waits for the one before it in its own
-                                const uint32_t word = y == 0 ? x[nb].x : y == 1 ? x[nb].y : y == 2 ? x[nb].z : x[nb].w;
-                                mma_bf16(s[nb], q[4 * blk + y], codes2(__byte_perm(word, 0, 0x4140)),
-                                         codes2(__byte_perm(word, 0, 0x4342)));
+                            for (int pb = 0; pb < 2; ++pb) {
+                                const uint4 &u = y[2 * pb], &v = y[2 * pb + 1];
+                                const uint32_t u1 = k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
+                                const uint32_t v1 = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
+                                const uint32_t ak[4] = {codes2(__byte_perm(u1, 0, 0x4140)), codes2(__byte_perm(v1, 0, 0x4140)),
+                                                        codes2(__byte_perm(u1, 0, 0x4342)), codes2(__byte_perm(v1, 0, 0x4342))};
+#pragma unroll
+                                for (int x = 0; x < X; ++x) mma_bf16(s[pb][x], ak, q[4 * blk + k][x][0], q[4 * blk + k][x][1]);
                             }
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int p = 16 * i + (lane >> 4) * 8 + (lane & 7), ch = 2 * (k & 3) + ((lane >> 3) & 1);
-                            uint32_t bk[4];
-                            ldsm4(ka + (k >> 2) * kRwChunk * 128 + p * 128 + ((ch ^ (p & 7)) << 4), bk);
-                            mma_bf16(s[2 * i], q[k], bk[0], bk[1]);
-                            mma_bf16(s[2 * i + 1], q[k], bk[2], bk[3]);
+                        for (int pb = 0; pb < 2; ++pb) {
+                            const int p = 16 * pb + ((lane >> 3) & 1) * 8 + (lane & 7), ch = 2 * (k & 3) + (lane >> 4);
+                            uint32_t ak[4];
+                            ldsm4(ka + (k >> 2) * kRwChunk * 128 + p * 128 + ((ch ^ (p & 7)) << 4), ak);
+#pragma unroll
+                            for (int x = 0; x < X; ++x) mma_bf16(s[pb][x], ak, q[k][x][0], q[k][x][1]);
                         }
                 }
-                // scores in the log2 domain
-#pragma unroll
-                for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float f = a.qscale;
-                        if constexpr (I8) f *= steps[nb * 8 + rw_slot<D, I8>(2 * kq + (c & 1))];
-                        s[nb][c] *= f;
-                    }
+                // scores in the log2 domain, the hidden ones out
                 const bool masked = t * kRwChunk + kRwChunk > vmin;
-                if (masked) {
+                const int p0 = t * kRwChunk + rw_slot<D, I8>(r8);
+                float top[X][2];
+                bool grows = false;
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb)
+                for (int x = 0; x < X; ++x)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (t * kRwChunk + nb * 8 + rw_slot<D, I8>(2 * kq + (c & 1)) >= vend[c >> 1]) s[nb][c] = -INFINITY;
-                }
-                float top[2];
+                    for (int j = 0; j < 2; ++j) {
+                        float y = -INFINITY;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    top[x] = s[0][2 * x];
+                        for (int pb = 0; pb < 2; ++pb)
 #pragma unroll
-                    for (int nb = 0; nb < 4; ++nb) top[x] = fmaxf(top[x], fmaxf(s[nb][2 * x], s[nb][2 * x + 1]));
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-                    top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-                }
-                if (__any_sync(0xffffffffu, top[0] - m[0] > kPaMaxGrowth || top[1] - m[1] > kPaMaxGrowth)) {
-                    float alpha[2];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const float mn = fmaxf(m[x], top[x]);
-                        alpha[x] = m[x] == mn ? 1.0f : ex2(m[x] - mn);
-                        m[x] = mn;
-                        l[x] *= alpha[x];
+                            for (int h = 0; h < 2; ++h) {
+                                float& z = s[pb][x][2 * h + j];
+                                z *= I8 ? ks[pb][h] : a.qscale;
+                                if (masked && p0 + 16 * pb + 8 * h >= vend[x][j]) z = -INFINITY;
+                                y = fmaxf(y, z);
+                            }
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                        top[x][j] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                        grows |= top[x][j] - m[x][j] > kPaMaxGrowth;
                     }
+                if (__any_sync(0xffffffffu, grows)) {
 #pragma unroll
-                    for (int db = 0; db < D / 8; ++db)
+                    for (int x = 0; x < X; ++x)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) o[db][c] *= alpha[c >> 1];
-                }
-                const float ref[2] = {m[0] == -INFINITY ? 0.0f : m[0], m[1] == -INFINITY ? 0.0f : m[1]};
+                        for (int j = 0; j < 2; ++j) {
+                            const float mn = fmaxf(m[x][j], top[x][j]);
+                            const float alpha = m[x][j] == mn ? 1.0f : ex2(m[x][j] - mn);
+                            m[x][j] = mn;
+                            l[x][j] *= alpha;
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[nb][c] = ex2(s[nb][c] - ref[c >> 1]);
-                        l[c >> 1] += s[nb][c];
-                        if constexpr (I8) {
-                            const int p = nb * 8 + rw_slot<D, I8>(2 * kq + (c & 1));
-                            // (a step behind the last position may be anything)
-                            s[nb][c] = masked && t * kRwChunk + p >= vend[c >> 1] ? 0.0f : s[nb][c] * steps[kRwChunk + p];
+                            for (int db = 0; db < D / 16; ++db) {
+                                o[db][x][j] *= alpha;
+                                o[db][x][2 + j] *= alpha;
+                            }
                         }
-                    }
+                }
+                uint32_t p[2][X][2];  // the probabilities as the products' B operand
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    const float ref[2] = {m[x][0] == -INFINITY ? 0.0f : m[x][0], m[x][1] == -INFINITY ? 0.0f : m[x][1]};
+#pragma unroll
+                    for (int pb = 0; pb < 2; ++pb)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float e[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                e[j] = ex2(s[pb][x][2 * h + j] - ref[j]);
+                                l[x][j] += e[j];
+                                // (a step behind the last position may be anything)
+                                if constexpr (I8) e[j] = masked && p0 + 16 * pb + 8 * h >= vend[x][j] ? 0.0f : e[j] * vs[pb][h];
+                            }
+                            p[pb][x][h] = movm_t(pack_bf16x2(e[0], e[1]));
+                        }
+                }
                 if constexpr (!I8) {
                     const int valid = end - t * kRwChunk;
                     if (valid < kRwChunk) {
                         // values behind the last position that anything sees: zeros (probability zero times whatever
                         // the page holds there would not be)
                         for (int e = lane; e < (kRwChunk - valid) * 8 * (D / 64); e += 32) {
-                            const int h = e / ((kRwChunk - valid) * 8), x = e % ((kRwChunk - valid) * 8);
-                            *reinterpret_cast<uint4*>(vtile + h * kRwChunk * 128 + valid * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+                            const int h = e / ((kRwChunk - valid) * 8), y = e % ((kRwChunk - valid) * 8);
+                            *reinterpret_cast<uint4*>(vtile + h * kRwChunk * 128 + valid * 128 + y * 16) = make_uint4(0, 0, 0, 0);
                         }
                         __syncwarp();
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t p[4] = {pack_bf16x2(s[2 * k][0], s[2 * k][1]), pack_bf16x2(s[2 * k][2], s[2 * k][3]),
-                                           pack_bf16x2(s[2 * k + 1][0], s[2 * k + 1][1]),
-                                           pack_bf16x2(s[2 * k + 1][2], s[2 * k + 1][3])};
+                for (int pb = 0; pb < 2; ++pb) {
                     if constexpr (I8) {
                         constexpr int N = D / 32;  // words of a lane's run of D/8 dimensions
                         uint32_t v[4][N];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {  // slots 2 kq and 2 kq + 1 of both eights
-                            const int r = (2 * k + (x >> 1)) * 8 + rw_slot<D, I8>(2 * kq + (x & 1));
+                        for (int y = 0; y < 4; ++y) {  // slots 2 kq and 2 kq + 1 of both eights
+                            const int r = (2 * pb + (y >> 1)) * 8 + rw_slot<D, I8>(2 * kq + (y & 1));
                             if constexpr (D == 128) {
-                                const uint4 y = *reinterpret_cast<const uint4*>(vtile + r * D + ((r8 ^ (r & 7)) << 4));
-                                v[x][0] = y.x;
-                                v[x][1] = y.y;
-                                v[x][2] = y.z;
-                                v[x][3] = y.w;
+                                const uint4 z = *reinterpret_cast<const uint4*>(vtile + r * D + ((r8 ^ (r & 7)) << 4));
+                                v[y][0] = z.x;
+                                v[y][1] = z.y;
+                                v[y][2] = z.z;
+                                v[y][3] = z.w;
                             } else {
-                                const uint2 y = *reinterpret_cast<const uint2*>(vtile + r * D + r8 * 8);
-                                v[x][0] = y.x;
-                                v[x][1] = y.y;
+                                const uint2 z = *reinterpret_cast<const uint2*>(vtile + r * D + r8 * 8);
+                                v[y][0] = z.x;
+                                v[y][1] = z.y;
                             }
                         }
 #pragma unroll
-                        for (int db = 0; db < D / 8; ++db) {
-                            const uint32_t pick = (uint32_t)((db & 3) | ((4 + (db & 3)) << 8));  // its bytes 0 and 2
-                            mma_bf16(o[db], p, codes2(__byte_perm(v[0][db >> 2], v[1][db >> 2], pick)),
-                                     codes2(__byte_perm(v[2][db >> 2], v[3][db >> 2], pick)));
+                        for (int db = 0; db < D / 16; ++db) {
+                            uint32_t av[4];  // dimensions 2 db and 2 db + 1 of the run, both eights
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                const int b = 2 * db + (y & 1);
+                                const uint32_t pick = (uint32_t)((b & 3) | ((4 + (b & 3)) << 8));  // its bytes 0 and 2
+                                av[y] = codes2(__byte_perm(v[2 * (y >> 1)][b >> 2], v[2 * (y >> 1) + 1][b >> 2], pick));
+                            }
+#pragma unroll
+                            for (int x = 0; x < X; ++x) mma_bf16(o[db][x], av, p[pb][x][0], p[pb][x][1]);
                         }
                     } else {
 #pragma unroll
-                        for (int db = 0; db < D / 8; db += 2) {
-                            const int r = 16 * k + ((lane >> 3) & 1) * 8 + (lane & 7), ch = (db & 7) + (lane >> 4);
-                            uint32_t bv[4];
-                            ldsm4t(va + (db >> 3) * kRwChunk * 128 + r * 128 + ((ch ^ (r & 7)) << 4), bv);
-                            mma_bf16(o[db], p, bv[0], bv[1]);
-                            mma_bf16(o[db + 1], p, bv[2], bv[3]);
+                        for (int db = 0; db < D / 16; ++db) {
+                            const int r = 16 * pb + (lane >> 4) * 8 + (lane & 7), ch = 2 * (db & 3) + ((lane >> 3) & 1);
+                            uint32_t av[4];
+                            ldsm4t(va + (db >> 2) * kRwChunk * 128 + r * 128 + ((ch ^ (r & 7)) << 4), av);
+#pragma unroll
+                            for (int x = 0; x < X; ++x) mma_bf16(o[db][x], av, p[pb][x][0], p[pb][x][1]);
                         }
                     }
                 }
@@ -573,20 +625,21 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
             if (merges > 0) ok = __all_sync(0xffffffffu, mbar_wait(got_bar, (merges - 1) & 1u));  // the last item's are read
             if (!ok) break;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-                l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-                const int r = r8 + 8 * x;
-                if (r < rows) {
-                    if (kq == 0) ml[w * kRwRows + r] = make_float2(m[x], l[x]);
-                    float* dst = osm + (w * kRwRows + r) * D + 2 * kq;
-                    if (t0 + skip < t1) {
+            for (int x = 0; x < X; ++x)
 #pragma unroll
-                        for (int db = 0; db < D / 8; ++db)
-                            *reinterpret_cast<float2*>(dst + 8 * db) = make_float2(o[db][2 * x], o[db][2 * x + 1]);
+                for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                    for (int y = 4; y < 32; y *= 2) l[x][j] += __shfl_xor_sync(0xffffffffu, l[x][j], y);
+                    const int r = 8 * x + 2 * kq + j;
+                    if (r < rows && t0 + skip < t1) {
+                        if (r8 == 0) ml[w * NR + r] = make_float2(m[x][j], l[x][j]);
+#pragma unroll
+                        for (int db = 0; db < D / 16; ++db) {
+                            osm[(w * NR + r) * C::kOStride + 16 * db + r8] = o[db][x][j];
+                            osm[(w * NR + r) * C::kOStride + 16 * db + 8 + r8] = o[db][x][2 + j];
+                        }
                     }
                 }
-            }
             __syncwarp();
             if (lane == 0) mbar_arrive(put_bar);
             ok = __all_sync(0xffffffffu, mbar_wait(put_bar, merges & 1u));
@@ -602,7 +655,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                 float mx = -INFINITY, den = 0.0f, n_0 = 0.0f, n_1 = 0.0f;
 #pragma unroll
                 for (int y = 0; y < W; ++y) {
-                    v[y] = y < used ? ml[(done0 + y) % W * kRwRows + r] : make_float2(-INFINITY, 0.0f);
+                    v[y] = y < used ? ml[(done0 + y) % W * NR + r] : make_float2(-INFINITY, 0.0f);
                     mx = fmaxf(mx, v[y].x);
                 }
 #pragma unroll
@@ -610,7 +663,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8>::kThreads, 1) attn_rows_kernel(
                     const float f = v[y].x == -INFINITY ? 0.0f : ex2(v[y].x - mx);
                     den = fmaf(f, v[y].y, den);
                     if (y < used) {
-                        const float* src = osm + ((done0 + y) % W * kRwRows + r) * D;
+                        const float* src = osm + ((done0 + y) % W * NR + r) * C::kOStride;
                         n_0 = fmaf(f, src[rw_column<D, I8>(d)], n_0);
                         n_1 = fmaf(f, src[rw_column<D, I8>(d + 1)], n_1);
                     }

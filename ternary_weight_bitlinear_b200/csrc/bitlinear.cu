@@ -903,7 +903,7 @@ PagedWs attn_paged_ws(int64_t T, int64_t group, int64_t head_dim, int sms) {
 // Few rows against each position (attn_rows.cuh): 16 a sequence and key/value
 // head on average.  (The lengths themselves are on the device: either kernel
 // is right for every batch.)
-template <int D, bool I8>
+template <int D, bool I8, int NR>
 bl_status attn_rows_launch(PagedAttnArgs& a, int dev, const DeviceInfo& info, unsigned long long* counters,
                            cudaStream_t stream) {
     CUtensorMap map_k, map_v;
@@ -914,11 +914,11 @@ bl_status attn_rows_launch(PagedAttnArgs& a, int dev, const DeviceInfo& info, un
     if (!make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw) ||
         !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw))
         return BL_ERR_CUDA;
-    using C = RwCfg<D, I8>;
-    if (prepare_kernel(reinterpret_cast<const void*>(attn_rows_kernel<D, I8>), dev, info, C::kThreads, C::kSmem) < 0)
+    using C = RwCfg<D, I8, NR>;
+    if (prepare_kernel(reinterpret_cast<const void*>(attn_rows_kernel<D, I8, NR>), dev, info, C::kThreads, C::kSmem) < 0)
         return BL_ERR_CUDA;
     a.part_rows = kRwRows;
-    return launch(attn_rows_kernel<D, I8>, dim3((unsigned)info.sms), dim3(C::kThreads), (size_t)C::kSmem, stream, map_k,
+    return launch(attn_rows_kernel<D, I8, NR>, dim3((unsigned)info.sms), dim3(C::kThreads), (size_t)C::kSmem, stream, map_k,
                   map_v, (const PagedAttnArgs&)a, counters, next_epoch());
 }
 
@@ -934,8 +934,10 @@ bl_status attn_paged_launch(PagedAttnArgs& a, void* workspace, int dev, const De
     a.tokens = kPaRows / a.group;
     a.box = kPaTile;
     while (a.c.page_size % a.box != 0) a.box /= 2;
-    if ((int64_t)a.b.T * a.group <= (int64_t)kRwRows * a.b.batch)
-        return attn_rows_launch<D, I8>(a, dev, info, reinterpret_cast<unsigned long long*>(ws), stream);
+    const int64_t rows = (int64_t)a.b.T * a.group;
+    unsigned long long* counters = reinterpret_cast<unsigned long long*>(ws);
+    if (rows <= (int64_t)8 * a.b.batch) return attn_rows_launch<D, I8, 8>(a, dev, info, counters, stream);
+    if (rows <= (int64_t)16 * a.b.batch) return attn_rows_launch<D, I8, 16>(a, dev, info, counters, stream);
     CUtensorMap map_q, map_k, map_v;
     const int64_t qd[4] = {D, a.group, a.b.T, a.c.kv_heads}, qs[3] = {D, a.q_stride, (int64_t)a.group * D};
     const int qb[4] = {64, a.group, a.tokens, 1};

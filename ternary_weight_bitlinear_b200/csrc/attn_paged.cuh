@@ -237,57 +237,81 @@ __device__ __forceinline__ void pa_share(int64_t total, int64_t* u0, int64_t* u1
 constexpr int kPaPlanWords = 7;
 template <class Cut>
 __device__ __forceinline__ void pa_plan(const PagedAttnArgs& a, int64_t* plan, KvSeq* seq, int64_t* warp_sums) {
-    const int nthr = blockDim.x;
-    int64_t total = 0, mine = 0, upto = 0;
+    int64_t total = 0, mine = 0, upto = 0, per = 0;
     KvSeq s = {0, 0, 0};
     auto units = [&](int b) {
-        if (b >= a.b.batch) return (int64_t)0;
-        s = kv_seq(a.b, b);
-        return pa_seq_units<Cut>(a, s) * a.c.kv_heads;
+        per = 0;
+        if (b < a.b.batch) {
+            s = kv_seq(a.b, b);
+            per = pa_seq_units<Cut>(a, s);
+        }
+        return per * a.c.kv_heads;
     };
+    // the thread whose sequence b holds unit u0 leaves the plan
+    auto locate = [&](int b, int64_t u0) {
+        if (mine > 0 && u0 >= upto - mine && u0 < upto) {
+            int64_t at = upto - mine;
+            const int g = total < (1 << 22) ? (int)((uint32_t)(u0 - at) / (uint32_t)per) : (int)((u0 - at) / per);
+            at += g * per;
+            int i = 0;
+            for (;;) {
+                const int c = Cut::cost(a, s, i);
+                if (u0 < at + c) break;
+                at += c;
+                ++i;
+            }
+            plan[2] = at;
+            plan[3] = b;
+            plan[4] = g;
+            plan[5] = i;
+            *seq = s;
+        }
+    };
+    int64_t u0, u1;
+    const auto leave = [&]() {
+        if (threadIdx.x == 0) {
+            plan[0] = u0;
+            plan[1] = u1;
+            plan[6] = total;
+            if (u0 >= u1) plan[2] = u1;  // nothing
+        }
+    };
+    if (a.b.batch <= 32) {  // one warp's work: the others need not be waited for in between
+        if (threadIdx.x < 32) {
+            const int lane = threadIdx.x;
+            mine = upto = units(lane);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            total = __shfl_sync(0xffffffffu, upto, 31);
+            pa_share(total, &u0, &u1);
+            leave();
+            if (u0 < u1) locate(lane, u0);
+        }
+        __syncthreads();
+        return;
+    }
+    const int nthr = blockDim.x;
     for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
         mine = units(b0 + threadIdx.x);
         int64_t sum;
         upto = total + pa_scan(mine, warp_sums, &sum);
         total += sum;
     }
-    int64_t u0, u1;
     pa_share(total, &u0, &u1);
-    const bool once = a.b.batch <= nthr;  // else the sequences are passed over again
-    if (threadIdx.x == 0) {
-        plan[0] = u0;
-        plan[1] = u1;
-        plan[6] = total;
-        if (u0 >= u1) plan[2] = u1;  // nothing
-    }
+    leave();
     if (u0 < u1) {
         int64_t sum = 0;
         for (int b0 = 0; b0 < a.b.batch; b0 += nthr) {
-            const int b = b0 + threadIdx.x;
-            if (!once) {
-                mine = units(b);
+            if (a.b.batch > nthr) {  // the sequences are passed over again
+                mine = units(b0 + threadIdx.x);
                 int64_t all;
                 upto = sum + pa_scan(mine, warp_sums, &all);
                 sum += all;
             }
-            if (mine > 0 && u0 >= upto - mine && u0 < upto) {
-                int64_t at = upto - mine;
-                const int64_t per = pa_seq_units<Cut>(a, s);
-                const int g = total < (1 << 22) ? (int)((uint32_t)(u0 - at) / (uint32_t)per) : (int)((u0 - at) / per);
-                at += g * per;
-                int i = 0;
-                for (;;) {
-                    const int c = Cut::cost(a, s, i);
-                    if (u0 < at + c) break;
-                    at += c;
-                    ++i;
-                }
-                plan[2] = at;
-                plan[3] = b;
-                plan[4] = g;
-                plan[5] = i;
-                *seq = s;
-            }
+            locate(b0 + threadIdx.x, u0);
         }
     }
     __syncthreads();

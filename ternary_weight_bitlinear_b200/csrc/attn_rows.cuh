@@ -22,8 +22,8 @@
 //  * Items ((sequence, head, 16 rows) times their chunks) are shared out
 //    evenly over the CTAs as in attn_paged.cuh.  The warps of a CTA merge
 //    through shared memory; of the CTAs that hold parts of one item the last
-//    to arrive merges them, in the order of the CTAs (so the result does not
-//    depend on which it is).  One launch.
+//    to arrive merges them (in groups where there are many), in the order of
+//    the CTAs, so the result does not depend on which it is.  One launch.
 #pragma once
 
 #include "attn_paged.cuh"
@@ -34,6 +34,9 @@ constexpr int kRwRows = 16;       // most rows of an item
 constexpr int kRwChunk = 32;      // positions of a chunk
 constexpr int kRwItemUnits = 4;   // cost of an item beside its chunks, in chunks
 constexpr int kRwItems = 4;       // ring of items
+constexpr int kRwGroup = 16;      // parts of an item that one CTA merges at once, where there are more than kRwAlone
+constexpr int kRwAlone = 32;
+constexpr int kRwCounters = 3;    // counters a CTA
 
 // NR: rows of an item, 8 or 16.
 template <int D, bool I8, int NR>
@@ -168,8 +171,14 @@ struct RwWalk {
     }
 };
 
-__device__ __forceinline__ void st_release(unsigned long long* p, unsigned long long v) {
-    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+__device__ __forceinline__ void st_counter(unsigned long long* p, unsigned long long v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+// An arrival: releases what this thread (and those it synchronised with) wrote, acquires what earlier ones released.
+__device__ __forceinline__ unsigned long long arrive_counter(unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("atom.acq_rel.gpu.global.add.u64 %0, [%1], 1;" : "=l"(v) : "l"(p) : "memory");
+    return v;
 }
 __device__ __forceinline__ unsigned long long ld_acquire(const unsigned long long* p) {
     unsigned long long v;
@@ -277,8 +286,9 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    // this CTA's counter, for an item that begins here and goes on in others: this launch's, and nothing counted yet
-    if (threadIdx.x == 0) st_release(counters + blockIdx.x, epoch << 32);
+    // this CTA's counters (an item that begins here and goes on in others; a group that its parts are first of): this
+    // launch's, and nothing counted yet
+    if (threadIdx.x < 3) st_counter(threadIdx.x == 0 ? counters + blockIdx.x : counters + gridDim.x + 2 * blockIdx.x + threadIdx.x - 1, epoch << 32);
     pa_plan<RwCut<NR>>(a, plan, seq, warp_sums);
 
     bool ok = true;
@@ -304,7 +314,18 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
         RwItem it;
         for (bool more = true; more; ++ii) {
             more = walk.next(it);
-            if (!more) it.b = -1;
+            if (!more) {
+                it.b = -1;
+                it.t0 = it.t1 = 0;
+            }
+            // the page table's next 32 entries, a lane each, and the 32 after them (on their way while the first are used)
+            const int32_t* table = a.b.pages + (int64_t)it.b * a.b.max_pages;
+            const int pages = more ? a.c.by_page.div(it.end + a.c.page_size - 1) : 0;
+            auto entries = [&](int at) { return at + lane < pages ? __ldcg(table + at + lane) : -1; };
+            const int skip = (int)((ld + C::kLoaders - n0 % C::kLoaders) % C::kLoaders);
+            const uint32_t n = n0;  // the item's first chunk
+            int p0 = a.c.by_page.div((it.t0 + skip) * kRwChunk);
+            int now = entries(p0), next = entries(p0 + 32);
             if (ld == 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(iempty_bar(ii), ((ii / kRwItems) & 1u) ^ 1u));
                 if (!ok) break;
@@ -315,15 +336,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                 __syncwarp();
             }
             if (!more) break;
-            // the page table's next 32 entries, a lane each, and the 32 after them (on their way while the first are used)
-            const int32_t* table = a.b.pages + (int64_t)it.b * a.b.max_pages;
-            const int pages = a.c.by_page.div(it.end + a.c.page_size - 1);
-            auto entries = [&](int at) { return at + lane < pages ? __ldcg(table + at + lane) : -1; };
-            const int skip = (int)((ld + C::kLoaders - n0 % C::kLoaders) % C::kLoaders);
-            const uint32_t n = n0;  // the item's first chunk
             n0 += it.t1 - it.t0;
-            int p0 = a.c.by_page.div((it.t0 + skip) * kRwChunk);
-            int now = entries(p0), next = entries(p0 + 32);
             for (int t = it.t0 + skip; t < it.t1; t += C::kLoaders) {
                 // lane x: box x of the chunk (which spans at most two pages)
                 const int p = t * kRwChunk + lane * box;
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
         const int w = ct >> 5, r8 = lane >> 2, kq = lane & 3;
         float* osm = reinterpret_cast<float*>(sm + C::kOffO);
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
-        bool begun = false;  // (consumer 0) an item begins here and goes on in other CTAs: the last of them resets the counter
+        int used_ctr = 0;  // counters of this CTA that others arrive at (the last of them resets it)
         uint32_t n0 = 0, merges = 0, sent = 0, told = 0;  // chunks passed; phases of the barriers
         while (const RwItem* item = take()) {
             const int t0 = item->t0, t1 = item->t1, rows = item->rows, end = item->end;
@@ -716,93 +729,114 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
             }
             ++merges;
             if (!whole) {
-                // ---- the last CTA with a part of the item merges them ----
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sent_bar);
-                ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
-                if (!ok) break;
-                ++sent;
-                if (ct == 0) {
-                    __threadfence();
-                    // once the CTA that the item begins in has set its counter for this launch (it was started
-                    // before this one, and set it first of all): chunks counted so far
-                    unsigned long long* ctr = counters + item->cta0;
-                    bool mine = false;
-                    for (int tries = 0; tries < (1 << 20) && !mine; ++tries) mine = ld_acquire(ctr) >> 32 == (epoch & 0xFFFFFFFFull);
-                    if (!mine) atomicOr(&g_status, kStatusTimeout);
-                    const unsigned chunks = (unsigned)(t1 - t0);
-                    const bool last = mine && (unsigned)(atomicAdd(ctr, (unsigned long long)chunks) & 0xFFFFFFFFull) + chunks == (unsigned)item->nt;
-                    // no count is left behind: a captured launch is replayed with its epoch
-                    if (last) st_release(ctr, 0);
-                    *last_flag = last;
-                    begun |= t0 == 0;
-                    mbar_arrive(told_bar);
-                }
-                __syncwarp();
-                ok = __all_sync(0xffffffffu, mbar_wait(told_bar, told & 1u));
-                if (!ok) break;
-                ++told;
-                if (*last_flag) {
-                    __threadfence();
-                    const int parts = item->parts, cta0 = item->cta0;
-                    const int64_t unit0 = ((int64_t)item->unit_hi << 32) | (uint32_t)item->unit_lo;
-                    const int64_t total = plan[6];
-                    auto part_of = [&](int y) {  // row block of part y: slot 1 of the CTA the item begins in, slot 0 of the others
-                        const int x = item->spread ? rw_cta_of(unit0 + y, total) : cta0 + y;
-                        return ((int64_t)x * 2 + (y == 0 ? 1 : 0)) * kRwRows;
-                    };
-                    constexpr int DL = D / 32;
-                    for (int r = w; r < rows; r += W) {
-                        float mx = -INFINITY;
-                        for (int y = lane; y < parts; y += 32) mx = fmaxf(mx, __ldcg(a.part_ml + (part_of(y) + r) * 2));
-                        mx = warp_max_f(mx);
-                        float den = 0.0f, num[DL] = {};
-                        for (int y0 = 0; y0 < parts; y0 += 32) {
-                            float f = 0.0f, fl = 0.0f;
-                            int64_t from = 0;
-                            if (y0 + lane < parts) {
-                                from = part_of(y0 + lane) + r;
-                                const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + from * 2));
-                                f = v.x == -INFINITY ? 0.0f : ex2(v.x - mx);
-                                fl = f * v.y;
-                            }
-                            den += warp_sum_f(fl);
-                            const int count = min(32, parts - y0);
-                            for (int y = 0; y < count; y += 8) {  // 8 vectors on their way at once
-                                float v[8][DL];
-#pragma unroll
-                                for (int z = 0; z < 8; ++z) {
-                                    const float* src = a.part + __shfl_sync(0xffffffffu, from, y + z) * D + lane * DL;
-                                    if (y + z < count) {
-                                        if constexpr (DL == 4)
-                                            *reinterpret_cast<float4*>(v[z]) = __ldcg(reinterpret_cast<const float4*>(src));
-                                        else
-                                            *reinterpret_cast<float2*>(v[z]) = __ldcg(reinterpret_cast<const float2*>(src));
-                                    }
-                                }
-#pragma unroll
-                                for (int z = 0; z < 8; ++z) {
-                                    const float fz = __shfl_sync(0xffffffffu, f, y + z);
-                                    if (y + z < count) {
-#pragma unroll
-                                        for (int e = 0; e < DL; ++e) num[e] = fmaf(fz, v[z][e], num[e]);
-                                    }
-                                }
-                            }
+                // ---- merge the item's parts over the CTAs ----
+                // Up to kRwAlone parts: the last CTA to arrive merges them.  More: the last of each kRwGroup neighbours
+                // merges those into the first one's place, and the last group's merges the groups.
+                const int parts = item->parts, cta0 = item->cta0;
+                const int groups = parts > kRwAlone ? (parts + kRwGroup - 1) / kRwGroup : 1;
+                const int64_t unit0 = ((int64_t)item->unit_hi << 32) | (uint32_t)item->unit_lo, total = plan[6];
+                // place of part y: slot 1 of the CTA the item begins in, slot 0 of the others
+                auto place = [&](int y) {
+                    const int x = item->spread ? rw_cta_of(unit0 + y, total) : cta0 + y;
+                    return 2 * x + (y == 0 ? 1 : 0);
+                };
+                // This CTA arrives at a counter of the launch; whether it is the last of `count`.  The counter was set
+                // by its CTA, which was started before this one and set it first of all: an arrival that still finds
+                // another launch's value is overwritten by that, and made again.
+                auto arrive_last = [&](unsigned long long* ctr, int count) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sent_bar);
+                    ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
+                    ++sent;
+                    if (!ok) return false;
+                    if (ct == 0) {
+                        const unsigned long long tag = epoch & 0xFFFFFFFFull;
+                        unsigned long long old = arrive_counter(ctr);
+                        for (int tries = 0; old >> 32 != tag && tries < 64; ++tries) {
+                            for (int spin = 0; spin < (1 << 16) && ld_acquire(ctr) >> 32 != tag; ++spin) {}
+                            old = arrive_counter(ctr);
                         }
-                        const int row = item->row0 + r, tok = a.by_group.div(row);
-                        const int ve = a.causal ? item->vbase + tok + 1 : item->len;
-                        uint16_t* dst = a.out + (int64_t)(item->q0 + tok) * a.o_stride + (head0 + a.by_group.mod(row)) * D + lane * DL;
-#pragma unroll
-                        for (int e = 0; e < DL; e += 2)
-                            *reinterpret_cast<uint32_t*>(dst + e) = ve > 0 ? pack_bf16x2(num[e] / den, num[e + 1] / den) : 0u;
+                        if (old >> 32 != tag) atomicOr(&g_status, kStatusTimeout);
+                        const bool last = old >> 32 == tag && (int)(old & 0xFFFFFFFFull) + 1 == count;
+                        if (last) st_counter(ctr, 0);  // nothing is left behind: a captured launch is replayed with its epoch
+                        *last_flag = last;
+                        mbar_arrive(told_bar);
                     }
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, mbar_wait(told_bar, told & 1u));
+                    ++told;
+                    return ok && *last_flag;
+                };
+                constexpr int DL = D / 32;
+                // parts first, first + step, ... (count of them), a row by a warp: into the place of the first (again a
+                // part), or normalised into out
+                auto merge_parts = [&](int first, int step, int count, bool final) {
+                    for (int r = w; r < rows; r += W) {
+                        float mx = -INFINITY, den = 0.0f, num[DL] = {};
+                        for (int y0 = 0; y0 < count; y0 += kRwGroup) {
+                            const int64_t from = (int64_t)place(first + min(y0 + (lane & (kRwGroup - 1)), count - 1) * step) * kRwRows + r;
+                            float v[kRwGroup][DL];
+#pragma unroll
+                            for (int z = 0; z < kRwGroup; ++z) {
+                                const float* src = a.part + __shfl_sync(0xffffffffu, from, z) * D + lane * DL;
+                                if constexpr (DL == 4)
+                                    *reinterpret_cast<float4*>(v[z]) = __ldcg(reinterpret_cast<const float4*>(src));
+                                else
+                                    *reinterpret_cast<float2*>(v[z]) = __ldcg(reinterpret_cast<const float2*>(src));
+                            }
+                            float2 y = __ldcg(reinterpret_cast<const float2*>(a.part_ml + from * 2));
+                            if (y0 + (lane & (kRwGroup - 1)) >= count) y = make_float2(-INFINITY, 0.0f);
+                            const float mn = fmaxf(mx, warp_max_f(y.x));
+                            const float f = y.x == -INFINITY ? 0.0f : ex2(y.x - mn);
+                            const float keep = mx == -INFINITY ? 0.0f : ex2(mx - mn);
+                            den = fmaf(den, keep, warp_sum_f(lane < kRwGroup ? f * y.y : 0.0f));
+#pragma unroll
+                            for (int e = 0; e < DL; ++e) num[e] *= keep;
+#pragma unroll
+                            for (int z = 0; z < kRwGroup; ++z) {
+                                const float fz = __shfl_sync(0xffffffffu, f, z);
+                                if (y0 + z < count) {
+#pragma unroll
+                                    for (int e = 0; e < DL; ++e) num[e] = fmaf(fz, v[z][e], num[e]);
+                                }
+                            }
+                            mx = mn;
+                        }
+                        if (final) {
+                            const int row = item->row0 + r, tok = a.by_group.div(row);
+                            const int ve = a.causal ? item->vbase + tok + 1 : item->len;
+                            uint16_t* dst = a.out + (int64_t)(item->q0 + tok) * a.o_stride + (head0 + a.by_group.mod(row)) * D + lane * DL;
+#pragma unroll
+                            for (int e = 0; e < DL; e += 2)
+                                *reinterpret_cast<uint32_t*>(dst + e) = ve > 0 ? pack_bf16x2(num[e] / den, num[e + 1] / den) : 0u;
+                        } else {
+                            const int64_t at = (int64_t)place(first) * kRwRows + r;
+#pragma unroll
+                            for (int e = 0; e < DL; ++e) a.part[at * D + lane * DL + e] = num[e];
+                            if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mx, den);
+                        }
+                    }
+                };
+                used_ctr |= t0 == 0 ? 1 : 0;
+                bool final = true;
+                if (groups > 1) {
+                    const int mine = item->spread ? t0 : (int)blockIdx.x - cta0, head = mine / kRwGroup * kRwGroup;
+                    const int count = min(kRwGroup, parts - head);
+                    used_ctr |= mine == head ? (mine == 0 ? 4 : 2) : 0;
+                    final = arrive_last(counters + gridDim.x + place(head), count);
+                    if (final) merge_parts(head, 1, count, false);
                 }
+                if (final && ok && arrive_last(counters + cta0, groups > 1 ? groups : parts))
+                    merge_parts(0, groups > 1 ? kRwGroup : 1, groups > 1 ? groups : parts, true);
+                if (!ok) break;
             }
             release();
         }
-        if (ct == 0 && !begun) st_release(counters + blockIdx.x, 0);
+        if (ct == 0) {  // counters of this CTA that nobody arrives at
+            if (!(used_ctr & 1)) st_counter(counters + blockIdx.x, 0);
+            if (!(used_ctr & 2)) st_counter(counters + gridDim.x + 2 * blockIdx.x, 0);
+            if (!(used_ctr & 4)) st_counter(counters + gridDim.x + 2 * blockIdx.x + 1, 0);
+        }
     }
     __syncthreads();
 }

@@ -894,6 +894,7 @@ PagedWs attn_paged_ws(int64_t T, int64_t group, int64_t head_dim, int sms) {
     PagedWs w;
     w.part_rows = T <= tokens ? T * group : 2 * kPaRows;  // rows of an item: one sub-tile, or two
     w.part_rows = std::max<int64_t>(w.part_rows, kRwRows);
+    static_assert(kRwCounters * sizeof(unsigned long long) <= 2 * sizeof(int4), "a CTA's counters lie where its descriptions do");
     w.desc_bytes = ((int64_t)sms * 2 * sizeof(int4) + 255) / 256 * 256;
     w.ml_bytes = ((int64_t)sms * 2 * w.part_rows * 8 + 255) / 256 * 256;
     w.bytes = w.desc_bytes + w.ml_bytes + (int64_t)sms * 2 * w.part_rows * head_dim * 4;

@@ -15,11 +15,13 @@
 // step, so every reader of that row (and no other) gets NaN.
 //
 // Both kernels move each row once and are bound by HBM bytes (for a few rows
-// by latency: the row's sequence, its length and its page are three dependent
-// loads).  A group of d/8 lanes takes one (row, head): 16 bytes a lane, both
-// the key and the value in flight before the lookups begin; the row's
+// by latency).  A group of d/8 lanes takes one or four (row, head) pairs, 16 bytes a
+// lane; a warp looks up 32 sequences at once, a lane each, so a row costs two
+// rounds of dependent loads (its sequence, its page) before its own; the row's
 // maximum costs log2(d/8) shuffles.
 #pragma once
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -101,22 +103,43 @@ __device__ __forceinline__ int kv_page(const KvCacheArgs& c, const KvBatchArgs& 
     return -1;
 }
 
-// Where this group's row lies in the cache: element offset of (page, slot,
-// head) and of its step; false when the row has no place.
-__device__ __forceinline__ bool kv_place(const KvCacheArgs& c, const KvBatchArgs& a, int t, int head,
-                                         int b, int64_t* off, int64_t* step_off) {
-    while (b < a.batch && __ldcg(a.cu_q + b + 1) <= t) ++b;  // this group's row may be a later one than the warp's first
-    if (b >= a.batch) return false;
-    const KvSeq s = kv_seq(a, b);
-    const int pos = s.len - s.n + (t - s.q0);
-    if (t < s.q0 || pos < 0) return false;
-    const int page = kv_page(c, a, b, pos);
-    if (page < 0) return false;
-    const int slot = c.by_page.mod(pos);
-    *off = page * c.sp + slot * c.ss + head * c.sh;
-    *step_off = ((int64_t)page * c.kv_heads + head) * c.page_size + slot;
-    return true;
-}
+// 32 neighbouring sequences, one a lane of a warp.
+struct KvWindow {
+    int base, next;  // the window's first sequence; where this lane's sequence ends in the arrays (as it stands there)
+    KvSeq s;
+    // The window that holds the sequence of row t (the warp's first): with up to 32 sequences there is one only.
+    __device__ __forceinline__ KvWindow(const KvBatchArgs& a, int t, int lane) {
+        base = a.batch <= 32 ? 0 : min(kv_seq_of_row(a, t, lane), a.batch - 1);
+        const bool have = base + lane < a.batch;
+        next = have ? __ldcg(a.cu_q + base + lane + 1) : INT32_MAX;
+        s = {0, 0, 0};
+        if (have) s = kv_seq(a, base + lane);
+    }
+    // Where row t lies in the cache (element offset of (page, slot, head) and of its step); false when it has no place.
+    // Every lane of the warp calls it, each with its own row.
+    __device__ __forceinline__ bool place(const KvCacheArgs& c, const KvBatchArgs& a, int t, int head, int64_t* off,
+                                          int64_t* step_off) const {
+        int i = 0;  // sequences of the window that end at or before t (the ends ascend)
+#pragma unroll
+        for (int step = 16; step > 0; step >>= 1)
+            if (__shfl_sync(0xffffffffu, next, i + step - 1) <= t) i += step;
+        const bool past = __shfl_sync(0xffffffffu, next, i) <= t;  // behind the window
+        KvSeq q = {__shfl_sync(0xffffffffu, s.q0, i), __shfl_sync(0xffffffffu, s.n, i), __shfl_sync(0xffffffffu, s.len, i)};
+        int b = base + i;
+        if (past) {
+            while (b < a.batch && __ldcg(a.cu_q + b + 1) <= t) ++b;
+            if (b < a.batch) q = kv_seq(a, b);
+        }
+        const int pos = q.len - q.n + (t - q.q0);
+        if (b >= a.batch || t < q.q0 || t >= q.q0 + q.n || pos < 0) return false;
+        const int page = kv_page(c, a, b, pos);
+        if (page < 0) return false;
+        const int slot = c.by_page.mod(pos);
+        *off = page * c.sp + slot * c.ss + head * c.sh;
+        *step_off = ((int64_t)page * c.kv_heads + head) * c.page_size + slot;
+        return true;
+    }
+};
 
 // Largest |x| of eight bf16 values, as bf16 bits (above every finite value
 // when one is an infinity or NaN).
@@ -128,17 +151,22 @@ __device__ __forceinline__ uint32_t kv_absmax8(const uint4& x) {
     return max(m & 0xFFFFu, m >> 16);
 }
 
-// Eight codes of one row's scale.
+// Eight codes of one row's scale.  Adding 1.5 2^23 rounds to an integer (ties
+// to even, as rint) and leaves it in two's complement in the low bits, without
+// the slower conversion instructions; |x s| <= 127 (1 + 2^-23), so the clamp at
+// -128 never binds.
 __device__ __forceinline__ uint2 kv_codes8(const uint4& x, float s) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t r[2] = {0, 0};
+    uint32_t c[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float f = bf16_bits_to_float((w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-        const int c = min(max(__float2int_rn(__fmul_rn(f, s)), -128), 127);
-        r[i >> 2] |= (uint32_t)(c & 0xFF) << (8 * (i & 3));
+        const float f = __uint_as_float((i & 1) ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+        c[i] = __float_as_uint(__fadd_rn(__fmul_rn(f, s), 12582912.0f));
     }
-    return make_uint2(r[0], r[1]);
+    auto four = [&](int i) {
+        return __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
+    };
+    return make_uint2(four(0), four(4));
 }
 
 // One row quantised by its group of LANES lanes.
@@ -154,76 +182,109 @@ __device__ __forceinline__ void kv_store_i8(const uint4& x, int8_t* dst, float* 
     if (part == 0) *step = finite ? __frcp_rn(s) : __int_as_float(0x7FC00000);
 }
 
-template <int D, bool I8>
+// R rows a group, GROUPS apart, so neighbouring groups have neighbouring heads
+// and tokens.
+template <int D, bool I8, int R>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCacheArgs c, const KvBatchArgs a,
                                                               const uint16_t* __restrict__ k, int64_t k_stride,
                                                               const uint16_t* __restrict__ v, int64_t v_stride) {
     constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
     const int lane = threadIdx.x & 31, part = threadIdx.x % LANES;
-    const int64_t pairs = (int64_t)a.T * c.kv_heads;
-    const int64_t warp_pair = (int64_t)blockIdx.x * GROUPS + (threadIdx.x & ~31) / LANES;
-    const int64_t pair = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES;
+    const int pairs = a.T * c.kv_heads;  // (row, head) pairs
+    const int block0 = blockIdx.x * (GROUPS * R);
+    const int warp0 = block0 + (threadIdx.x & ~31) / LANES, first = block0 + threadIdx.x / LANES;
     pdl_wait();
     pdl_launch_dependents();
-    if (warp_pair >= pairs) return;  // warp-uniform
-    const bool have = pair < pairs;
-    const int t = (int)((have ? pair : warp_pair) / c.kv_heads), head = (int)((have ? pair : warp_pair) % c.kv_heads);
-    const uint4 kx = __ldcg(reinterpret_cast<const uint4*>(k + t * k_stride + head * D) + part);
-    const uint4 vx = __ldcg(reinterpret_cast<const uint4*>(v + t * v_stride + head * D) + part);
-    const int b = kv_seq_of_row(a, (int)(warp_pair / c.kv_heads), lane);
-    int64_t off = 0, step_off = 0;
-    const bool live = have && kv_place(c, a, t, head, b, &off, &step_off);
-    if constexpr (I8) {
-        kv_store_i8<LANES>(kx, static_cast<int8_t*>(c.k) + off, c.k_step + step_off, part, live);
-        kv_store_i8<LANES>(vx, static_cast<int8_t*>(c.v) + off, c.v_step + step_off, part, live);
-    } else if (live) {
-        *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.k) + off) + part) = kx;
-        *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.v) + off) + part) = vx;
+    if (warp0 >= pairs) return;  // warp-uniform
+    uint4 kx[R], vx[R];
+    int t[R], head[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        const int pair = min(first + u * GROUPS, pairs - 1);
+        t[u] = c.by_heads.div(pair);
+        head[u] = pair - t[u] * c.kv_heads;
+        kx[u] = __ldcg(reinterpret_cast<const uint4*>(k + t[u] * k_stride + head[u] * D) + part);
+        vx[u] = __ldcg(reinterpret_cast<const uint4*>(v + t[u] * v_stride + head[u] * D) + part);
+    }
+    const KvWindow window(a, c.by_heads.div(warp0), lane);
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        int64_t off = 0, step_off = 0;
+        const bool live = window.place(c, a, t[u], head[u], &off, &step_off) && first + u * GROUPS < pairs;
+        if constexpr (I8) {
+            kv_store_i8<LANES>(kx[u], static_cast<int8_t*>(c.k) + off, c.k_step + step_off, part, live);
+            kv_store_i8<LANES>(vx[u], static_cast<int8_t*>(c.v) + off, c.v_step + step_off, part, live);
+        } else if (live) {
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.k) + off) + part) = kx[u];
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.v) + off) + part) = vx[u];
+        }
     }
 }
 
-// Eight bf16 values of eight codes: RN_bf16(RN32(code * step)).
+// Eight bf16 values of eight codes: RN_bf16(RN32(code * step)).  A code with its
+// sign bit flipped is code + 128 >= 0: as the low byte of the binary32 2^23 it
+// makes 2^23 + 128 + code, exactly.
 __device__ __forceinline__ uint4 kv_values8(const uint2& c, float step) {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t w = (i < 2 ? c.x : c.y) >> (16 * (i & 1));
-        const float lo = __fmul_rn((float)(int8_t)(w & 0xFF), step);
-        const float hi = __fmul_rn((float)(int8_t)((w >> 8) & 0xFF), step);
-        r[i] = pack_bf16x2(lo, hi);
+        const uint32_t w = (i < 2 ? c.x : c.y) ^ 0x80808080u;
+        const float lo = __uint_as_float(__byte_perm(w, 0x4B000000u, (i & 1) ? 0x7442 : 0x7440));
+        const float hi = __uint_as_float(__byte_perm(w, 0x4B000000u, (i & 1) ? 0x7443 : 0x7441));
+        r[i] = pack_bf16x2(__fmul_rn(__fsub_rn(lo, 8388736.0f), step), __fmul_rn(__fsub_rn(hi, 8388736.0f), step));
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-template <int D, bool I8>
+template <int D, bool I8, int R>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCacheArgs c, const KvBatchArgs a,
                                                              uint16_t* __restrict__ k, int64_t k_stride,
                                                              uint16_t* __restrict__ v, int64_t v_stride) {
     constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
+    using Vec = typename std::conditional<I8, uint2, uint4>::type;  // eight elements as they are held
+    using Held = typename std::conditional<I8, int8_t, uint16_t>::type;
     const int lane = threadIdx.x & 31, part = threadIdx.x % LANES;
-    const int64_t pairs = (int64_t)a.T * c.kv_heads;
-    const int64_t warp_pair = (int64_t)blockIdx.x * GROUPS + (threadIdx.x & ~31) / LANES;
-    const int64_t pair = (int64_t)blockIdx.x * GROUPS + threadIdx.x / LANES;
+    const int pairs = a.T * c.kv_heads;
+    const int block0 = blockIdx.x * (GROUPS * R);
+    const int warp0 = block0 + (threadIdx.x & ~31) / LANES, first = block0 + threadIdx.x / LANES;
     pdl_wait();
     pdl_launch_dependents();
-    if (warp_pair >= pairs) return;
-    const int b = kv_seq_of_row(a, (int)(warp_pair / c.kv_heads), lane);
-    if (pair >= pairs) return;
-    const int t = (int)(pair / c.kv_heads), head = (int)(pair % c.kv_heads);
-    int64_t off, step_off;
-    if (!kv_place(c, a, t, head, b, &off, &step_off)) return;
-    uint4 kx, vx;
-    if constexpr (I8) {
-        const uint2 kc = __ldcg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(c.k) + off) + part);
-        const uint2 vc = __ldcg(reinterpret_cast<const uint2*>(static_cast<const int8_t*>(c.v) + off) + part);
-        kx = kv_values8(kc, __ldcg(c.k_step + step_off));
-        vx = kv_values8(vc, __ldcg(c.v_step + step_off));
-    } else {
-        kx = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.k) + off) + part);
-        vx = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(c.v) + off) + part);
+    if (warp0 >= pairs) return;
+    const KvWindow window(a, c.by_heads.div(warp0), lane);
+    Vec kx[R], vx[R];
+    float ks[R], vs[R];
+    int64_t to_k[R], to_v[R];
+    bool live[R];
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        const int pair = min(first + u * GROUPS, pairs - 1), t = c.by_heads.div(pair), head = pair - t * c.kv_heads;
+        int64_t off, step_off;
+        live[u] = window.place(c, a, t, head, &off, &step_off) && first + u * GROUPS < pairs;
+        if (live[u]) {
+            kx[u] = __ldcg(reinterpret_cast<const Vec*>(static_cast<const Held*>(c.k) + off) + part);
+            vx[u] = __ldcg(reinterpret_cast<const Vec*>(static_cast<const Held*>(c.v) + off) + part);
+            if constexpr (I8) {
+                ks[u] = __ldcg(c.k_step + step_off);
+                vs[u] = __ldcg(c.v_step + step_off);
+            }
+        }
+        to_k[u] = t * k_stride + head * D;
+        to_v[u] = t * v_stride + head * D;
     }
-    *(reinterpret_cast<uint4*>(k + t * k_stride + head * D) + part) = kx;
-    *(reinterpret_cast<uint4*>(v + t * v_stride + head * D) + part) = vx;
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+        if (!live[u]) continue;
+        uint4 x, y;
+        if constexpr (I8) {
+            x = kv_values8(kx[u], ks[u]);
+            y = kv_values8(vx[u], vs[u]);
+        } else {
+            x = kx[u];
+            y = vx[u];
+        }
+        *(reinterpret_cast<uint4*>(k + to_k[u]) + part) = x;
+        *(reinterpret_cast<uint4*>(v + to_v[u]) + part) = y;
+    }
 }
 
 }  // namespace bl

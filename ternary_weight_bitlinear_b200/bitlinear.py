@@ -5,7 +5,9 @@ torch tensors; all arithmetic runs in the library's kernels.  There is no
 fallback: if ``libbitlinear.so`` is missing or no sm_100 device is current,
 calls raise.
 """
+import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -103,11 +105,13 @@ class KvCache(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("k_step", _P), ("v_step", _P), ("num_pages", _I64), ("page_size", _I64),
                 ("kv_heads", _I64), ("head_dim", _I64), ("stride_page", _I64), ("stride_slot", _I64),
                 ("stride_head", _I64), ("format", _INT)]
+    shape = device = None  # (kv_heads, head_dim) and the tensors' device, from make_kv_cache
 
 
 class KvBatch(ctypes.Structure):
     """bl_kv_batch: the sequences of one step (see make_kv_batch)."""
     _fields_ = [("cu_q", _P), ("kv_len", _P), ("pages", _P), ("batch", _I64), ("max_pages", _I64)]
+    device = None
 
 
 class BitLinearError(RuntimeError):
@@ -393,29 +397,31 @@ def bitlinear_attn_decode(q, k_cache, v_cache, L, q_heads, kv_heads, scale, out=
 
 
 # --- paged key/value cache --------------------------------------------------------
+# (Called once a layer and token: the marshalling is kept short.)
 def make_kv_cache(k_pages, v_pages, k_step=None, v_step=None):
     """A bl_kv_cache of k_pages, v_pages [num_pages, page_size, kv_heads, head_dim]
     (any strides, the same for both, head_dim contiguous), bf16, or int8 with
     fp32 steps k_step, v_step [num_pages, kv_heads, page_size].  Holds its tensors."""
-    i8 = isinstance(k_pages, torch.Tensor) and k_pages.dtype == torch.int8
-    for t in (k_pages, v_pages):
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == (torch.int8 if i8 else torch.bfloat16)
-                and t.dim() == 4):
-            raise TypeError("k_pages and v_pages must be CUDA tensors of four dimensions, both bfloat16 or both int8")
-    strides = k_pages.stride()
-    if v_pages.shape != k_pages.shape or v_pages.stride() != strides or strides[3] != 1:
-        raise TypeError("k_pages and v_pages must have the same shape and strides, with head_dim contiguous")
-    n, page, heads, d = k_pages.shape
+    dtype = k_pages.dtype
+    i8 = dtype == torch.int8
+    strides, shape, dev = k_pages.stride(), k_pages.shape, k_pages.device
+    if not (k_pages.is_cuda and len(shape) == 4 and (i8 or dtype == torch.bfloat16)):
+        raise TypeError("k_pages and v_pages must be CUDA tensors of four dimensions, both bfloat16 or both int8")
+    if v_pages.dtype != dtype or v_pages.device != dev or v_pages.shape != shape or v_pages.stride() != strides \
+            or strides[3] != 1:
+        raise TypeError("k_pages and v_pages must have the same type, device, shape and strides, with head_dim contiguous")
+    n, page, heads, d = shape
     if i8:
         for t in (k_step, v_step):
-            if _need(t, torch.float32, "the steps of an int8 cache", 3).shape != (n, heads, page):
-                raise TypeError("k_step and v_step must be [num_pages, kv_heads, page_size]")
+            if _need(t, torch.float32, "the steps of an int8 cache", 3).shape != (n, heads, page) or t.device != dev:
+                raise TypeError("k_step and v_step must be [num_pages, kv_heads, page_size], on the pages' device")
     elif k_step is not None or v_step is not None:
         raise TypeError("a bfloat16 cache has no steps")
-    _same_device(k_pages, v_pages, k_step, v_step)
     c = KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_step), _addr(v_step), n, page, heads, d,
                 strides[0], strides[1], strides[2], BL_KV_I8 if i8 else BL_KV_BF16)
     c.tensors = (k_pages, v_pages, k_step, v_step)
+    c.device = dev
+    c.shape = (heads, d)
     return c
 
 
@@ -426,39 +432,28 @@ def make_kv_batch(cu_q, kv_len, pages):
     _need(kv_len, torch.int32, "kv_len", 1)
     _need(pages, torch.int32, "pages", 2)
     batch, max_pages = pages.shape
-    if cu_q.numel() != batch + 1 or kv_len.numel() != batch:
+    dev = pages.device
+    if cu_q.shape[0] != batch + 1 or kv_len.shape[0] != batch:
         raise TypeError("cu_q must have batch + 1 entries, kv_len batch and pages batch rows")
-    _same_device(cu_q, kv_len, pages)
+    if cu_q.device != dev or kv_len.device != dev:
+        raise TypeError("cu_q, kv_len and pages must be on one device")
     b = KvBatch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), batch, max_pages)
     b.tensors = (cu_q, kv_len, pages)
+    b.device = dev
     return b
 
 
-def _same_device(*tensors):
-    index = None
-    for t in tensors:
-        if t is not None:
-            i = t.device.index
-            if index is not None and i != index:
-                raise TypeError("the tensors of one call must be on one device")
-            index = i
-    return index
-
-
-def _kv_rows(t, d, name):
-    """(heads, elements between rows) of bf16 rows [T, heads, head_dim] or
+def _kv_rows(t, d, name, dev):
+    """(rows, heads, elements between rows) of bf16 rows [T, heads, head_dim] or
     [T, heads * head_dim], heads contiguous, rows with any stride."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.bfloat16 and t.dim() in (2, 3)):
-        raise TypeError("%s must be a CUDA torch.bfloat16 tensor of two or three dimensions" % name)
-    s, n = t.stride(), t.shape
+    n = t.shape
+    if t.dtype != torch.bfloat16 or t.device != dev or not 2 <= len(n) <= 3:
+        raise TypeError("%s must be a torch.bfloat16 tensor of two or three dimensions, on the cache's device" % name)
+    s = t.stride()
     width = n[1] if len(n) == 2 else n[1] * n[2]
     if s[-1] != 1 or width % d or (len(n) == 3 and (n[2] != d or (n[1] > 1 and s[1] != d))):
         raise TypeError("%s must have rows of contiguous heads of %d" % (name, d))
-    return width // d, (s[0] if n[0] > 1 else width)
-
-
-def _kv_stream(device, stream):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    return n[0], width // d, (s[0] if n[0] > 1 else width)
 
 
 def _kv_new(make, stream):
@@ -469,60 +464,71 @@ def _kv_new(make, stream):
         return make()
 
 
-def _on_device(device, call):
-    """call() with `device` current (the library works on the current device)."""
-    if device == torch.cuda.current_device():
-        return call()
-    with torch.cuda.device(device):
-        return call()
+def _kv_call(fn, cache, batch, stream, *args):
+    """The entry point `fn` on the stream (None: the device's current one), with
+    the cache's device current, as the library needs it."""
+    dev = cache.device
+    if batch.device != dev:
+        raise TypeError("the cache and the batch must be on one device")
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        status = getattr(lib(), fn)(ctypes.byref(cache), ctypes.byref(batch), *args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib(), fn)(ctypes.byref(cache), ctypes.byref(batch), *args, raw)
+    if status != 0:
+        raise BitLinearError(fn, status)
 
 
 def bitlinear_kv_write(k, v, cache, batch, stream=None):
     """New rows k, v (bf16 [T, kv_heads, head_dim], rows with any stride) into the
     pages of a make_kv_cache() at the places of a make_kv_batch(); quantised per
     row when the cache is int8."""
-    d = cache.head_dim
-    hk, sk = _kv_rows(k, d, "k")
-    hv, sv = _kv_rows(v, d, "v")
-    if hk != cache.kv_heads or hv != hk or v.shape[0] != k.shape[0]:
+    heads, d = cache.shape
+    T, hk, sk = _kv_rows(k, d, "k", cache.device)
+    Tv, hv, sv = _kv_rows(v, d, "v", cache.device)
+    if hk != heads or hv != heads or Tv != T:
         raise TypeError("k and v must be [T, kv_heads, head_dim]")
-    dev = _same_device(k, v, cache.tensors[0], batch.tensors[0])
-    _check("bitlinear_kv_write", _on_device(dev, lambda: lib().bitlinear_kv_write(
-        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), sk, v.data_ptr(), sv, k.shape[0],
-        _kv_stream(dev, stream))))
+    _kv_call("bitlinear_kv_write", cache, batch, stream, k.data_ptr(), sk, v.data_ptr(), sv, T)
 
 
 def bitlinear_kv_read(cache, batch, T=None, k=None, v=None, stream=None):
     """The rows of a batch read back out of the cache: (k, v) bf16 [T, kv_heads,
     head_dim], into the given tensors or new ones of T rows.  Rows of no sequence
     are left as they were (in a new tensor: zeros)."""
-    d, heads = cache.head_dim, cache.kv_heads
-    if T is None:
-        if k is None and v is None:
-            raise TypeError("bitlinear_kv_read needs T, k or v")
-        T = (v if k is None else k).shape[0]
+    heads, d = cache.shape
+    if k is None or v is None:
+        if T is None:
+            if k is None and v is None:
+                raise TypeError("bitlinear_kv_read needs T, k or v")
+            T = (v if k is None else k).shape[0]
 
-    def new():
-        return torch.zeros((T, heads, d), dtype=torch.bfloat16, device=cache.tensors[0].device)
+        def new():
+            return torch.zeros((T, heads, d), dtype=torch.bfloat16, device=cache.device)
 
-    k = _kv_new(new, stream) if k is None else k
-    v = _kv_new(new, stream) if v is None else v
-    hk, sk = _kv_rows(k, d, "k")
-    hv, sv = _kv_rows(v, d, "v")
-    if hk != heads or hv != hk or v.shape[0] != T or k.shape[0] != T:
+        k = _kv_new(new, stream) if k is None else k
+        v = _kv_new(new, stream) if v is None else v
+    Tk, hk, sk = _kv_rows(k, d, "k", cache.device)
+    Tv, hv, sv = _kv_rows(v, d, "v", cache.device)
+    if hk != heads or hv != heads or Tv != Tk or (T is not None and T != Tk):
         raise TypeError("k and v must be [T, kv_heads, head_dim]")
-    dev = _same_device(k, v, cache.tensors[0], batch.tensors[0])
-    _check("bitlinear_kv_read", _on_device(dev, lambda: lib().bitlinear_kv_read(
-        ctypes.byref(cache), ctypes.byref(batch), k.data_ptr(), sk, v.data_ptr(), sv, T,
-        _kv_stream(dev, stream))))
+    _kv_call("bitlinear_kv_read", cache, batch, stream, k.data_ptr(), sk, v.data_ptr(), sv, Tk)
     return k, v
 
 
-def bitlinear_attn_paged_workspace_size(T, q_heads, kv_heads, head_dim):
+@functools.lru_cache(maxsize=4096)
+def _attn_paged_workspace(T, q_heads, kv_heads, head_dim, device):
     n = ctypes.c_size_t()
-    _check("bitlinear_attn_paged_workspace_size",
-           lib().bitlinear_attn_paged_workspace_size(T, q_heads, kv_heads, head_dim, ctypes.byref(n)))
+    with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
+        _check("bitlinear_attn_paged_workspace_size",
+               lib().bitlinear_attn_paged_workspace_size(T, q_heads, kv_heads, head_dim, ctypes.byref(n)))
     return n.value
+
+
+def bitlinear_attn_paged_workspace_size(T, q_heads, kv_heads, head_dim):
+    """Bytes of workspace on the current device."""
+    return _attn_paged_workspace(T, q_heads, kv_heads, head_dim,
+                                 torch.cuda.current_device() if torch.cuda.is_available() else None)
 
 
 def bitlinear_attn_paged(q, cache, batch, scale, causal=True, out=None, workspace=None, stream=None):
@@ -530,26 +536,21 @@ def bitlinear_attn_paged(q, cache, batch, scale, causal=True, out=None, workspac
     any stride) over the paged cache, which holds their own keys and values
     already: bf16, the shape of q.  Rows of no sequence are left as they were (in
     a new tensor: zeros)."""
-    d = cache.head_dim
-    heads, sq = _kv_rows(q, d, "q")
+    kv_heads, d = cache.shape
+    dev = cache.device
+    T, heads, sq = _kv_rows(q, d, "q", dev)
     if out is None:
-        out = _kv_new(lambda: torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device), stream)
-    ho, so = _kv_rows(out, d, "out")
-    T = q.shape[0]
-    if ho != heads or out.shape[0] != T:
+        out = _kv_new(lambda: torch.zeros(q.shape, dtype=torch.bfloat16, device=dev), stream)
+    To, ho, so = _kv_rows(out, d, "out", dev)
+    if ho != heads or To != T:
         raise TypeError("out must have the shape of q")
-    dev = _same_device(q, out, cache.tensors[0], batch.tensors[0], workspace)
-
-    def call():
-        ws = workspace
-        if ws is None:
-            nbytes = bitlinear_attn_paged_workspace_size(T, heads, cache.kv_heads, d)
-            ws = _kv_new(lambda: _workspace(nbytes, q.device), stream)
-        return lib().bitlinear_attn_paged(
-            ctypes.byref(cache), ctypes.byref(batch), q.data_ptr(), sq, T, heads, scale, 1 if causal else 0,
-            out.data_ptr(), so, ws.data_ptr(), ws.numel() * ws.element_size(), _kv_stream(dev, stream))
-
-    _check("bitlinear_attn_paged", _on_device(dev, call))
+    if workspace is None:
+        nbytes = _attn_paged_workspace(T, heads, kv_heads, d, dev.index)
+        workspace = _kv_new(lambda: torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev), stream)
+    elif workspace.device != dev:
+        raise TypeError("the workspace must be on the cache's device")
+    _kv_call("bitlinear_attn_paged", cache, batch, stream, q.data_ptr(), sq, T, heads, scale, 1 if causal else 0,
+             out.data_ptr(), so, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
 
 

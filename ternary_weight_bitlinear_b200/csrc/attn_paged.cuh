@@ -414,6 +414,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Registers moved between the warpgroups of a CTA (every warp of a group calls it).
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
@@ -442,6 +449,29 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
         "mov.b64 A, {%0, %1};\n\tmov.b64 B, {%2, %3};\n\t"
         "add.rn.f32x2 A, A, B;\n\tmov.b64 {%0, %1}, A;\n\t}"
         : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
+}
+
+// 2^x of two finite or -infinite x <= 127 on the FMA and integer pipes, beside
+// the special-function unit's ex2: with n = round(x), f = x - n in [-1/2, 1/2],
+// 2^f by a polynomial of degree four (its constant term 1, its other
+// coefficients fitted here for the least largest relative error: 2.9e-6 in
+// binary32) and n added to the exponent.  x below -127 (scores far under the
+// maximum, hidden ones at -infinity) counts as -127, which comes out as 0.
+__device__ __forceinline__ void ex2_poly2(float& x, float& y) {
+    x = fmaxf(x, -127.0f);
+    y = fmaxf(y, -127.0f);
+    float tx = x, ty = y;
+    add2(tx, ty, 12582912.0f, 12582912.0f);  // 1.5 2^23: n in the low bits
+    float nx = tx, ny = ty;
+    add2(nx, ny, -12582912.0f, -12582912.0f);
+    fma2(nx, ny, -1.0f, -1.0f, x, y);        // f
+    float px = 0x1.39f3a6p-7f, py = 0x1.39f3a6p-7f;
+    fma2(px, py, nx, ny, 0x1.c9fb52p-5f, 0x1.c9fb52p-5f);
+    fma2(px, py, nx, ny, 0x1.ec03b6p-3f, 0x1.ec03b6p-3f);
+    fma2(px, py, nx, ny, 0x1.62e132p-1f, 0x1.62e132p-1f);
+    fma2(px, py, nx, ny, 1.0f, 1.0f);
+    x = __uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23));
+    y = __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23));
 }
 
 // ---- one row by a warp, position by position --------------------------------
@@ -855,34 +885,52 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     tc_fence_after();
                 }
                 if (mine && warp_live) {
-                    float s[kPaTile];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32u * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
-                    tmem_ld_wait();
-                    if constexpr (I8) {
-#pragma unroll
-                        for (int c = 0; c < kPaTile; c += 4) {
-                            const float4 k4 = *reinterpret_cast<const float4*>(ks + c);
-                            mul2(s[c], s[c + 1], k4.x, k4.y);
-                            mul2(s[c + 2], s[c + 3], k4.z, k4.w);
-                        }
-                    }
                     const int vis = vend - t * kPaTile;  // columns that this row sees
                     const bool masked = __any_sync(0xffffffffu, vis < kPaTile);
-                    if (masked) {
+                    // Scores as they are needed twice (for the maximum, then for the probabilities): a bf16 cache's row
+                    // stays in registers; an int8 cache's is read from tensor memory again, its steps leave no room.
+                    float s[I8 ? 32 : kPaTile];
+                    auto load = [&](int c, float* r) {
+                        tmem_ld32_nowait(ts + 32u * c, reinterpret_cast<uint32_t*>(r));
+                    };
+                    auto prepare = [&](int c, float* r) {  // times the steps, without the hidden columns
+                        if constexpr (I8) {
 #pragma unroll
-                        for (int c = 0; c < kPaTile; ++c)
-                            if (c >= vis) s[c] = -INFINITY;
-                    }
-                    float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * c + e);
+                                mul2(r[e], r[e + 1], k4.x, k4.y);
+                                mul2(r[e + 2], r[e + 3], k4.z, k4.w);
+                            }
+                        }
+                        if (masked) {
 #pragma unroll
-                    for (int c = 4; c < kPaTile; c += 4) {
-                        x0 = fmaxf(x0, s[c]);
-                        x1 = fmaxf(x1, s[c + 1]);
-                        x2 = fmaxf(x2, s[c + 2]);
-                        x3 = fmaxf(x3, s[c + 3]);
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * c + e >= vis) r[e] = -INFINITY;
+                        }
+                    };
+                    float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+                    if constexpr (!I8) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) load(c, s + 32 * c);
+                        tmem_ld_wait();
                     }
-                    const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float* r = I8 ? s : s + 32 * c;
+                        if constexpr (I8) {
+                            load(c, r);
+                            tmem_ld_wait();
+                        }
+                        prepare(c, r);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            x0 = max3_nan(x0, r[e], r[e + 1]);
+                            x1 = max3_nan(x1, r[e + 2], r[e + 3]);
+                            x2 = max3_nan(x2, r[e + 4], r[e + 5]);
+                            x3 = max3_nan(x3, r[e + 6], r[e + 7]);
+                        }
+                    }
+                    const float top = max3_nan(x0, x1, max3_nan(x2, x3, x3));
                     if (first) {
                         m = top;
                     } else if (__any_sync(0xffffffffu, live && (top - m) * a.qscale > kPaMaxGrowth)) {
@@ -901,36 +949,54 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     }
                     first = false;
                     const float off = m == -INFINITY ? 0.0f : -m * a.qscale;
+                    // half of the exponentials by polynomial: the special-function unit alone takes as long as the
+                    // tile's products.  Infinities above and NaN only it knows.
+                    const bool plain = __all_sync(0xffffffffu, !live || top < INFINITY);
                     float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-                    for (int c = 0; c < kPaTile; c += 2) {
-                        fma2(s[c], s[c + 1], a.qscale, a.qscale, off, off);
-                        s[c] = ex2(s[c]);
-                        s[c + 1] = ex2(s[c + 1]);
-                        add2(l0, l1, s[c], s[c + 1]);
-                    }
-                    l += l0 + l1;
-                    if constexpr (I8) {
-                        const float* vs = ks + kPaTile;
-#pragma unroll
-                        for (int c = 0; c < kPaTile; c += 4) {
-                            const float4 v4 = *reinterpret_cast<const float4*>(vs + c);
-                            mul2(s[c], s[c + 1], v4.x, v4.y);
-                            mul2(s[c + 2], s[c + 3], v4.z, v4.w);
-                        }
-                        if (masked) {  // a step behind the last position may be anything
-#pragma unroll
-                            for (int c = 0; c < kPaTile; ++c)
-                                if (c >= vis) s[c] = 0.0f;
-                        }
-                    }
-#pragma unroll
                     for (int c = 0; c < 4; ++c) {
+                        float* r = I8 ? s : s + 32 * c;
+                        if constexpr (I8) {
+                            load(c, r);
+                            tmem_ld_wait();
+                            prepare(c, r);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) fma2(r[e], r[e + 1], a.qscale, a.qscale, off, off);
+                        if (plain) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                r[e] = ex2(r[e]);
+                                r[e + 1] = ex2(r[e + 1]);
+                                ex2_poly2(r[e + 2], r[e + 3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[e] = ex2(r[e]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) add2(l0, l1, r[e], r[e + 1]);
+                        if constexpr (I8) {
+                            const float* vs = ks + kPaTile + 32 * c;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float4 v4 = *reinterpret_cast<const float4*>(vs + e);
+                                mul2(r[e], r[e + 1], v4.x, v4.y);
+                                mul2(r[e + 2], r[e + 3], v4.z, v4.w);
+                            }
+                            if (masked) {  // a step behind the last position may be anything
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * c + e >= vis) r[e] = 0.0f;
+                            }
+                        }
+                        // the probabilities over columns of scores that have been read
                         uint32_t pk[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]);
+                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(r[2 * e], r[2 * e + 1]);
                         tmem_st16(ts + 16u * c, pk);
                     }
+                    l += l0 + l1;
                     tmem_st_wait();
                 }
                 if (!I8 && mine && valid < kPaTile && valid % 16 != 0) {

@@ -9,7 +9,7 @@
 // prompts, on the tensor cores:
 //  * Tiles.  A sub-tile is 128 rows of one sequence and key/value head: 128 /
 //    group tokens times the group's heads, so keys and values are read once
-//    for the group.  Per tile of 128 positions S = Q K^T and O += P V are
+//    for the group.  Per step of 64 positions S = Q K^T and O += P V are
 //    tcgen05.mma (M = 128) with S, P (bf16, over S's columns) and O in tensor
 //    memory; a softmax thread owns a row: no shuffles.
 //  * Work.  An item is two sub-tiles (or a sequence's last, single one) of one
@@ -20,10 +20,14 @@
 //    spreads over the GPU as well as many short ones.  An item cut by shares
 //    leaves (max, sum, vector) partials, merged by attn_merge_kernel in the
 //    order of the CTAs: results do not depend on timing.
-//  * Two softmax warpgroups.  In a pair item each has one sub-tile; in a
-//    single item they take alternate position tiles of the same rows and
-//    merge at the end.  While one works on its scores the tensor core runs the
-//    other's products: PV of a tile, then QK of the same group's next one.
+//  * Two softmax warpgroups, each working in steps of 64 positions with two
+//    score buffers: while it works on one step, the scores of its next are
+//    made and the probabilities of its last are multiplied with the values, so
+//    neither the group nor the tensor core waits for the other.  (A product of
+//    eight dependent instructions takes 790 cycles alone, 512 with another's
+//    between them.)  In a pair item each group has one sub-tile; in a single
+//    item each takes one half of every tile for the same rows, merged at the
+//    end.
 //  * Loads.  Pages arrive by TMA (a box per page part, no multicast) into a
 //    ring that holds K and V tiles in turn, running ahead across items.  int8
 //    pages land in a raw ring; a converter warpgroup writes their codes, exact
@@ -47,7 +51,8 @@
 namespace bl {
 
 constexpr int kPaRows = 128;     // rows of a sub-tile (MMA M)
-constexpr int kPaTile = 128;     // positions of a tile
+constexpr int kPaTile = 128;     // positions of a tile (a ring place)
+constexpr int kPaStep = 64;      // positions of a softmax step
 constexpr int kPaItemUnits = 1;  // cost of an item beside its tiles, in tiles of one sub-tile
 constexpr int kNoMask = 1 << 30;
 constexpr float kPaMaxGrowth = 8.0f;  // log2 growth of the maximum that a row's sums absorb
@@ -88,7 +93,7 @@ struct PaItem {
     int nsub;        // sub-tiles: 1 or 2
     int nt;          // position tiles of the item
     int t0, t1;      // those of this CTA
-    int nt0;         // tiles up to t1 that the first sub-tile sees
+    int end0;        // positions that some row of the first sub-tile sees
     int end;         // positions that some row of the item sees
     int vend;        // positions that its first token sees; below zero where it has no place
     int len;         // positions of the sequence
@@ -156,11 +161,11 @@ struct PaWalk {
             it.nt = nt;
             it.t0 = lo;
             it.t1 = hi;
-            it.nt0 = nsub == 2 ? min(hi, pa_tiles(pa_end(a, s, first + a.tokens))) : hi;
+            it.end0 = pa_end(a, s, min(first + a.tokens, s.n));
             it.end = pa_end(a, s, first + it.tokens);
             it.vend = a.causal ? s.len - s.n + first + 1 : s.len;
             it.len = s.len;
-            it.nq = lo == hi ? 0 : nsub == 2 && it.nt0 > lo ? 2 : 1;
+            it.nq = lo == hi ? 0 : nsub == 2 && it.end0 > lo * kPaTile ? 2 : 1;
             it.slot = slot;
             slot += it.nq;
             const bool mine = lo < hi || (nt == 0 && from <= 0);
@@ -337,8 +342,8 @@ struct PaCfg {
     static constexpr int kOffItems = kOffMl + kPaRows * 8;
     static constexpr int kOffBar = kOffItems + kPaItems * (int)sizeof(PaItem);
     // barriers: operand ring full/empty, raw full/empty, steps full/empty, Q full/empty,
-    // scores, probabilities, output done (one per group), merge full/empty, drain, items full/empty
-    static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kSteps + 4 + 6 + 2 + 2 + 2 * kPaItems;
+    // scores, probabilities, products with the values (a group's two buffers each), merge full/empty, drain, items full/empty
+    static constexpr int kBars = 2 * kStages + 2 * kRaw + 2 * kSteps + 4 + 12 + 2 + 2 + 2 * kPaItems;
     static constexpr int kOffPlan = kOffBar + 8 * kBars;
     static constexpr int kSmem = kOffPlan + 256 + 1024;       // plan words, alignment slack
     static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -375,9 +380,9 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
         : "memory");
 }
 
-// Instruction descriptors: binary32 accumulate, bf16 A and B, M = 128; N = 128
+// Instruction descriptors: binary32 accumulate, bf16 A and B, M = 128; N = 64
 // positions with B (keys) K-major, or N = D with B (values) N-major.
-constexpr uint32_t kPaIdescQk = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPaTile >> 3) << 17) |
+constexpr uint32_t kPaIdescQk = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kPaStep >> 3) << 17) |
                                 ((uint32_t)(kPaRows >> 4) << 24);
 template <int D>
 constexpr uint32_t pa_idesc_pv() {
@@ -414,13 +419,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// The largest of three; NaN if one is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // Registers moved between the warpgroups of a CTA (every warp of a group calls it).
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
@@ -449,29 +447,6 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
         "mov.b64 A, {%0, %1};\n\tmov.b64 B, {%2, %3};\n\t"
         "add.rn.f32x2 A, A, B;\n\tmov.b64 {%0, %1}, A;\n\t}"
         : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
-}
-
-// 2^x of two finite or -infinite x <= 127 on the FMA and integer pipes, beside
-// the special-function unit's ex2: with n = round(x), f = x - n in [-1/2, 1/2],
-// 2^f by a polynomial of degree four (its constant term 1, its other
-// coefficients fitted here for the least largest relative error: 2.9e-6 in
-// binary32) and n added to the exponent.  x below -127 (scores far under the
-// maximum, hidden ones at -infinity) counts as -127, which comes out as 0.
-__device__ __forceinline__ void ex2_poly2(float& x, float& y) {
-    x = fmaxf(x, -127.0f);
-    y = fmaxf(y, -127.0f);
-    float tx = x, ty = y;
-    add2(tx, ty, 12582912.0f, 12582912.0f);  // 1.5 2^23: n in the low bits
-    float nx = tx, ny = ty;
-    add2(nx, ny, -12582912.0f, -12582912.0f);
-    fma2(nx, ny, -1.0f, -1.0f, x, y);        // f
-    float px = 0x1.39f3a6p-7f, py = 0x1.39f3a6p-7f;
-    fma2(px, py, nx, ny, 0x1.c9fb52p-5f, 0x1.c9fb52p-5f);
-    fma2(px, py, nx, ny, 0x1.ec03b6p-3f, 0x1.ec03b6p-3f);
-    fma2(px, py, nx, ny, 0x1.62e132p-1f, 0x1.62e132p-1f);
-    fma2(px, py, nx, ny, 1.0f, 1.0f);
-    x = __uint_as_float(__float_as_uint(px) + (__float_as_uint(tx) << 23));
-    y = __uint_as_float(__float_as_uint(py) + (__float_as_uint(ty) << 23));
 }
 
 // ---- one row by a warp, position by position --------------------------------
@@ -533,15 +508,16 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     constexpr int kB2 = kB1 + 2 * C::kSteps;
     auto qfull_bar = [&](int s) { return bars + 8u * (kB2 + s); };
     auto qempty_bar = [&](int s) { return bars + 8u * (kB2 + 2 + s); };
-    auto score_bar = [&](int w) { return bars + 8u * (kB2 + 4 + w); };
-    auto prob_bar = [&](int w) { return bars + 8u * (kB2 + 6 + w); };
-    auto odone_bar = [&](int w) { return bars + 8u * (kB2 + 8 + w); };
-    const uint32_t mfull_bar = bars + 8u * (kB2 + 10), mempty_bar = bars + 8u * (kB2 + 11);
-    auto drain_bar = [&](int w) { return bars + 8u * (kB2 + 12 + w); };
-    const uint32_t item_bars = bars + 8u * (kB2 + 14);  // full, then empty
+    // step j of group w: buffer j & 1, phase j >> 1
+    auto score_bar = [&](int w, uint32_t j) { return bars + 8u * (kB2 + 4 + 2 * w + (j & 1)); };
+    auto prob_bar = [&](int w, uint32_t j) { return bars + 8u * (kB2 + 8 + 2 * w + (j & 1)); };
+    auto pv_bar = [&](int w, uint32_t j) { return bars + 8u * (kB2 + 12 + 2 * w + (j & 1)); };
+    const uint32_t mfull_bar = bars + 8u * (kB2 + 16), mempty_bar = bars + 8u * (kB2 + 17);
+    auto drain_bar = [&](int w) { return bars + 8u * (kB2 + 18 + w); };
+    const uint32_t item_bars = bars + 8u * (kB2 + 20);  // full, then empty
     auto ifull_bar = [&](uint32_t i) { return item_bars + 8u * (i % kPaItems); };
     auto iempty_bar = [&](uint32_t i) { return item_bars + 8u * (kPaItems + i % kPaItems); };
-    static_assert(kB2 + 14 + 2 * kPaItems == C::kBars, "barrier count");
+    static_assert(kB2 + 20 + 2 * kPaItems == C::kBars, "barrier count");
     PaItem* ring = reinterpret_cast<PaItem*>(sm + C::kOffItems);
     int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // kPaPlanWords
     int64_t* warp_sums = plan + 8;                                      // 16 words
@@ -565,10 +541,12 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         for (int s = 0; s < 2; ++s) {
             mbar_init(qfull_bar(s), 1);
             mbar_init(qempty_bar(s), 2);
-            mbar_init(score_bar(s), 1);
-            mbar_init(prob_bar(s), 4);
-            mbar_init(odone_bar(s), 1);
             mbar_init(drain_bar(s), 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(score_bar(s, j), 1);
+                mbar_init(prob_bar(s, j), 4);
+                mbar_init(pv_bar(s, j), 1);
+            }
         }
         mbar_init(mfull_bar, 4);
         mbar_init(mempty_bar, 4);
@@ -583,7 +561,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // columns: scores (and probabilities) of group w at 128 w, output of group w at 256 + 128 w
+    // columns: scores (and probabilities) of group w's step j at 128 w + 64 (j & 1), its output at 256 + 128 w
     pdl_wait();
     pdl_launch_dependents();
     pa_plan<PaCut>(a, plan, seq, warp_sums);
@@ -705,14 +683,14 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         }
     } else {
         // ---------------- MMA issuers: warp 1 + w for softmax group w ----------------
-        // In order: P V of the group's last tile (once its probabilities are there), then Q K^T of its next one into
-        // the same columns.  The two groups' chains fill each other's gaps on the tensor core.
+        // Two steps of a group are in flight: while its softmax works on one, the next one's scores are made in the other
+        // buffer, and the last one's probabilities are multiplied with the values.
         const int w = warp - 1;
         if (lane == 0) {
             const uint32_t sc = tmem + 128u * w, oc = tmem + 256u + 128u * w;
-            uint32_t n = 0, probs = 0;   // ring fills passed, probabilities waited for
-            struct { int st, ksteps; uint32_t ph; bool some, first, last; } pv;  // the tile whose P V is to come
-            pv.some = false;
+            uint32_t n = 0;               // ring fills passed
+            uint32_t made = 0, used = 0;  // steps whose scores (whose product with the values) are issued
+            uint32_t info[2] = {0, 0};    // of the steps between the two (see below)
             // Every group takes every fill of the rings in order, used or not: a phase's parity tells it from the ones
             // beside it alone.
             auto skip = [&]() {
@@ -722,30 +700,32 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                 ++n;
                 return true;
             };
-            auto finish = [&]() {  // O (+)= P V
-                pv.some = false;
-                if (!mbar_wait(full_bar(pv.st), pv.ph) || !mbar_wait(prob_bar(w), probs & 1u)) return false;
-                ++probs;
+            auto finish = [&]() {  // O (+)= P V of step `used`
+                const uint32_t x = used & 1 ? info[1] : info[0];
+                const int st = (int)(x & 0xFF), half = (int)(x >> 8) & 1, ksteps = (int)(x >> 12);
+                if (!mbar_wait(full_bar(st), (x >> 9) & 1u) || !mbar_wait(prob_bar(w, used), (used >> 1) & 1u)) return false;
                 tc_fence_after();
-                const uint64_t vd = pa_desc_v(base + C::kOffRing + pv.st * C::kTileBytes, C::kHalfBytes);
-                for (int k = 0; k < pv.ksteps; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
-                    tc_mma_f16_ts(oc, sc + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), !pv.first || k != 0);
-                tc_commit(empty_bar(pv.st));
-                if (pv.last) tc_commit(odone_bar(w));
+                const uint64_t vd = pa_desc_v(base + C::kOffRing + st * C::kTileBytes + half * (kPaStep * 128), C::kHalfBytes);
+                const uint32_t p = sc + 64u * (used & 1);
+                for (int k = 0; k < ksteps; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
+                    tc_mma_f16_ts(oc, p + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), !((x >> 10) & 1u) || k != 0);
+                tc_commit(pv_bar(w, used));
+                if ((x >> 11) & 1u) tc_commit(empty_bar(st));
+                ++used;
                 return true;
             };
             while (ok) {
                 ok = mbar_wait(ifull_bar(ii), (ii / kPaItems) & 1u);
                 if (!ok || ring[ii % kPaItems].b < 0) break;
                 const PaItem& it = ring[ii % kPaItems];
-                const int t0 = it.t0, t1 = it.t1, end = it.end, nt0 = it.nt0, nq = it.nq;
                 const bool pair = it.nsub == 2;
+                const int t0 = it.t0, t1 = it.t1, end = pair && w == 0 ? it.end0 : it.end, nq = it.nq;
                 const uint32_t slot = it.slot;
                 mbar_arrive(iempty_bar(ii));
                 ++ii;
-                // this group's tiles, and its Q tile (a single item's one is both groups')
-                const int from = pair ? t0 : t0 + w, to = pair && w == 0 ? nt0 : t1, step = pair ? 1 : 2;
+                // this group's Q tile (a single item's one is both groups')
                 const uint32_t own = slot + (nq == 2 ? w : 0);
+                const int from = 2 * t0 + (pair ? 0 : w), to = min(2 * t1, (end + kPaStep - 1) / kPaStep);  // its steps
                 for (int x = 0; ok && x < nq; ++x) {
                     const uint32_t q = slot + x;
                     ok = mbar_wait(qfull_bar((int)(q & 1)), (q >> 1) & 1u);
@@ -753,36 +733,41 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                 }
                 const uint64_t qd = smem_desc_sw128(base + (own & 1) * C::kTileBytes);
                 for (int t = t0; ok && t < t1; ++t) {
-                    if (pv.some && !(ok = finish())) break;
-                    if (t < from || t >= to || (t - from) % step != 0) {
-                        ok = skip() && skip();
+                    const int h0 = pair ? 0 : w, h1 = min(pair ? 2 : w + 1, to - 2 * t);  // its halves of the tile
+                    if (h0 >= h1) {
+                        while (ok && used != made) ok = finish();
+                        ok = ok && skip() && skip();
                         continue;
                     }
-                    const int st = (int)(n % NS);
-                    const uint64_t kd = smem_desc_sw128(base + C::kOffRing + st * C::kTileBytes);
-                    ok = mbar_wait(full_bar(st), (n / NS) & 1u);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int h = 0; h < C::kHalves; ++h)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {  // 16 dimensions (32 bytes) an instruction
-                            const uint64_t o = (uint64_t)((h * C::kHalfBytes + k * 32) >> 4);
-                            tc_mma_f16_ss(sc, qd + o, kd + o, kPaIdescQk, (h | k) != 0);
-                        }
-                    tc_commit(score_bar(w));
-                    tc_commit(empty_bar(st));
-                    pv.some = true;
-                    pv.st = (int)((n + 1) % NS);
-                    pv.ph = ((n + 1) / NS) & 1u;
-                    pv.ksteps = (min(kPaTile, end - t * kPaTile) + 15) / 16;
-                    pv.first = t == from;
-                    pv.last = t + step >= to;
+                    const int st = (int)(n % NS), vst = (int)((n + 1) % NS);
+                    const uint32_t ph = (n / NS) & 1u, vph = ((n + 1) / NS) & 1u;
                     n += 2;
-                    if (pv.last) tc_commit(qempty_bar((int)(own & 1)));
+                    for (int h = h0; h < h1; ++h) {
+                        if (made - used == 2 && !(ok = finish())) break;
+                        if (h == h0 && !(ok = mbar_wait(full_bar(st), ph))) break;
+                        tc_fence_after();
+                        const uint64_t kd = smem_desc_sw128(base + C::kOffRing + st * C::kTileBytes + h * (kPaStep * 128));
+                        const uint32_t s64 = sc + 64u * (made & 1);
+#pragma unroll
+                        for (int c = 0; c < C::kHalves; ++c)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {  // 16 dimensions (32 bytes) an instruction
+                                const uint64_t o = (uint64_t)((c * C::kHalfBytes + k * 32) >> 4);
+                                tc_mma_f16_ss(s64, qd + o, kd + o, kPaIdescQk, (c | k) != 0);
+                            }
+                        tc_commit(score_bar(w, made));
+                        if (h == h1 - 1) tc_commit(empty_bar(st));
+                        if (2 * t + h + (pair ? 1 : 2) >= to) tc_commit(qempty_bar((int)(own & 1)));
+                        const int valid = min(kPaStep, end - (2 * t + h) * kPaStep);
+                        const uint32_t x = (uint32_t)vst | (uint32_t)h << 8 | vph << 9 | (2 * t + h == from ? 1u << 10 : 0u) |
+                                           (h == h1 - 1 ? 1u << 11 : 0u) | (uint32_t)((valid + 15) / 16) << 12;
+                        if (made & 1) info[1] = x; else info[0] = x;
+                        ++made;
+                    }
                 }
-                // the item's last P V: the group's next tile may be items away, and need the ring place this one holds
-                if (ok && pv.some) ok = finish();
+                // the item's last products with the values: the group's next step may be items away, and need the ring
+                // place these hold
+                while (ok && used != made) ok = finish();
             }
             // every MMA this thread issued has finished before TMEM is freed
             tc_commit(drain_bar(w));
@@ -850,9 +835,9 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         const int row = quad * 32 + lane;
         const int tok = a.by_group.div(row), hh = a.by_group.mod(row);
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const uint32_t ts = tmem + lanes + 128u * w, to = tmem + lanes + 256u + 128u * w;
+        const uint32_t ts = tmem + lanes + 128u * w, to_o = tmem + lanes + 256u + 128u * w;
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
-        uint32_t seen = 0, done = 0, merges = 0, tile = 0;
+        uint32_t step = 0, merges = 0, tile = 0;  // steps of this group, merges, tiles
         int state = 0;      // of this CTA's first share (see desc)
         int4 began = make_int4(0, 0, 0, 0);
         while (const PaItem* item = take()) {
@@ -864,172 +849,146 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             const bool warp_live = quad * 32 < tokens * a.group;
             // positions that this row sees (a lane without a row is masked nowhere: its results go nowhere)
             const int vend = !live ? kNoMask : a.causal ? min(max(item->vend + sub * a.tokens + tok, 0), item->len) : item->len;
-            const int t_end = pair && w == 0 ? item->nt0 : t1;
+            const int to = min(2 * t1, ((pair && w == 0 ? item->end0 : end) + kPaStep - 1) / kPaStep);
+            const uint32_t step0 = step;
             float m = -INFINITY, l = 0.0f;
-            bool first = true;
             for (int t = t0; t < t1; ++t, ++tile) {
-                const bool mine = pair ? t < t_end : ((t - t0) & 1) == w;
                 const float* ks = nullptr;
-                const int valid = end - t * kPaTile;  // positions of the tile that some row sees
-                if constexpr (I8) {  // a tile of the other group's too: the ring's phases go by both
+                if constexpr (I8) {  // a tile without a step of this group too: the ring's phases go by both
                     const int ss = (int)(tile % C::kSteps);
                     ok = __all_sync(0xffffffffu, mbar_wait(sfull_bar(ss), (tile / C::kSteps) & 1u));
                     if (!ok) break;
                     ks = reinterpret_cast<const float*>(sm + C::kOffStep) + ss * 2 * kPaTile;
                 }
-                if (mine) {
-                    const bool got = mbar_wait(score_bar(w), seen & 1u);
-                    ok = __all_sync(0xffffffffu, got);
+                const int h1 = min(pair ? 2 : w + 1, to - 2 * t);
+                for (int h = pair ? 0 : w; h < h1; ++h, ++step) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(score_bar(w, step), (step >> 1) & 1u));
                     if (!ok) break;
-                    ++seen;
                     tc_fence_after();
-                }
-                if (mine && warp_live) {
-                    const int vis = vend - t * kPaTile;  // columns that this row sees
-                    const bool masked = __any_sync(0xffffffffu, vis < kPaTile);
-                    // Scores as they are needed twice (for the maximum, then for the probabilities): a bf16 cache's row
-                    // stays in registers; an int8 cache's is read from tensor memory again, its steps leave no room.
-                    float s[I8 ? 32 : kPaTile];
-                    auto load = [&](int c, float* r) {
-                        tmem_ld32_nowait(ts + 32u * c, reinterpret_cast<uint32_t*>(r));
-                    };
-                    auto prepare = [&](int c, float* r) {  // times the steps, without the hidden columns
+                    const int u = 2 * t + h;
+                    const int valid = end - u * kPaStep;  // positions of the step that some row of the item sees
+                    const uint32_t tb = ts + 64u * (step & 1);
+                    if (warp_live) {
+                        float s[kPaStep];
+                        tmem_ld32_nowait(tb, reinterpret_cast<uint32_t*>(s));
+                        tmem_ld32_nowait(tb + 32, reinterpret_cast<uint32_t*>(s) + 32);
+                        tmem_ld_wait();
                         if constexpr (I8) {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 k4 = *reinterpret_cast<const float4*>(ks + 32 * c + e);
-                                mul2(r[e], r[e + 1], k4.x, k4.y);
-                                mul2(r[e + 2], r[e + 3], k4.z, k4.w);
+                            for (int e = 0; e < kPaStep; e += 4) {
+                                const float4 k4 = *reinterpret_cast<const float4*>(ks + h * kPaStep + e);
+                                mul2(s[e], s[e + 1], k4.x, k4.y);
+                                mul2(s[e + 2], s[e + 3], k4.z, k4.w);
                             }
                         }
+                        const int vis = vend - u * kPaStep;  // columns that this row sees
+                        const bool masked = __any_sync(0xffffffffu, vis < kPaStep);
                         if (masked) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * c + e >= vis) r[e] = -INFINITY;
+                            for (int e = 0; e < kPaStep; ++e)
+                                if (e >= vis) s[e] = -INFINITY;
                         }
-                    };
-                    float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
-                    if constexpr (!I8) {
+                        float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) load(c, s + 32 * c);
-                        tmem_ld_wait();
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float* r = I8 ? s : s + 32 * c;
-                        if constexpr (I8) {
-                            load(c, r);
-                            tmem_ld_wait();
+                        for (int e = 4; e < kPaStep - 4; e += 8) {
+                            x0 = fmaxf(fmaxf(x0, s[e]), s[e + 1]);
+                            x1 = fmaxf(fmaxf(x1, s[e + 2]), s[e + 3]);
+                            x2 = fmaxf(fmaxf(x2, s[e + 4]), s[e + 5]);
+                            x3 = fmaxf(fmaxf(x3, s[e + 6]), s[e + 7]);
                         }
-                        prepare(c, r);
+                        x0 = fmaxf(fmaxf(x0, s[kPaStep - 4]), s[kPaStep - 3]);
+                        x1 = fmaxf(fmaxf(x1, s[kPaStep - 2]), s[kPaStep - 1]);
+                        const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+                        if (step == step0) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, live && (top - m) * a.qscale > kPaMaxGrowth)) {
+                            // the output so far to the new maximum, once the last step's product is in it
+                            ok = __all_sync(0xffffffffu, mbar_wait(pv_bar(w, step - 1), ((step - 1) >> 1) & 1u));
+                            if (!ok) break;
+                            tc_fence_after();
+                            const float mn = fmaxf(m, top);
+                            const float alpha = m == mn ? 1.0f : ex2((m - mn) * a.qscale);
+                            m = mn;
+                            l *= alpha;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            x0 = max3_nan(x0, r[e], r[e + 1]);
-                            x1 = max3_nan(x1, r[e + 2], r[e + 3]);
-                            x2 = max3_nan(x2, r[e + 4], r[e + 5]);
-                            x3 = max3_nan(x3, r[e + 6], r[e + 7]);
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(to_o + c, o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st32(to_o + c, o);
+                            }
                         }
-                    }
-                    const float top = max3_nan(x0, x1, max3_nan(x2, x3, x3));
-                    if (first) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, live && (top - m) * a.qscale > kPaMaxGrowth)) {
-                        const float mn = fmaxf(m, top);
-                        const float alpha = m == mn ? 1.0f : ex2((m - mn) * a.qscale);
-                        m = mn;
-                        l *= alpha;
+                        const float off = m == -INFINITY ? 0.0f : -m * a.qscale;
+                        float l0 = 0.0f, l1 = 0.0f, l2 = 0.0f, l3 = 0.0f;
 #pragma unroll
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + c, o);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(to + c, o);
-                        }
-                    }
-                    first = false;
-                    const float off = m == -INFINITY ? 0.0f : -m * a.qscale;
-                    // half of the exponentials by polynomial: the special-function unit alone takes as long as the
-                    // tile's products.  Infinities above and NaN only it knows.
-                    const bool plain = __all_sync(0xffffffffu, !live || top < INFINITY);
-                    float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float* r = I8 ? s : s + 32 * c;
-                        if constexpr (I8) {
-                            load(c, r);
-                            tmem_ld_wait();
-                            prepare(c, r);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) fma2(r[e], r[e + 1], a.qscale, a.qscale, off, off);
-                        if (plain) {
+                        for (int c = 0; c < 2; ++c) {
+                            float* r = s + 32 * c;
 #pragma unroll
                             for (int e = 0; e < 32; e += 4) {
-                                r[e] = ex2(r[e]);
-                                r[e + 1] = ex2(r[e + 1]);
-                                ex2_poly2(r[e + 2], r[e + 3]);
-                            }
-                        } else {
+                                fma2(r[e], r[e + 1], a.qscale, a.qscale, off, off);
+                                fma2(r[e + 2], r[e + 3], a.qscale, a.qscale, off, off);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = ex2(r[e]);
+                                for (int x = 0; x < 4; ++x) r[e + x] = ex2(r[e + x]);
+                                add2(l0, l1, r[e], r[e + 1]);
+                                add2(l2, l3, r[e + 2], r[e + 3]);
+                            }
+                            if constexpr (I8) {
+                                const float* vs = ks + kPaTile + h * kPaStep + 32 * c;
+#pragma unroll
+                                for (int e = 0; e < 32; e += 4) {
+                                    const float4 v4 = *reinterpret_cast<const float4*>(vs + e);
+                                    mul2(r[e], r[e + 1], v4.x, v4.y);
+                                    mul2(r[e + 2], r[e + 3], v4.z, v4.w);
+                                }
+                                if (masked) {  // a step behind the last position may be anything
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (32 * c + e >= vis) r[e] = 0.0f;
+                                }
+                            }
+                            // the probabilities over columns of scores that have been read
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(r[2 * e], r[2 * e + 1]);
+                            tmem_st16(tb + 16u * c, pk);
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) add2(l0, l1, r[e], r[e + 1]);
-                        if constexpr (I8) {
-                            const float* vs = ks + kPaTile + 32 * c;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) {
-                                const float4 v4 = *reinterpret_cast<const float4*>(vs + e);
-                                mul2(r[e], r[e + 1], v4.x, v4.y);
-                                mul2(r[e + 2], r[e + 3], v4.z, v4.w);
-                            }
-                            if (masked) {  // a step behind the last position may be anything
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (32 * c + e >= vis) r[e] = 0.0f;
-                            }
-                        }
-                        // the probabilities over columns of scores that have been read
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(r[2 * e], r[2 * e + 1]);
-                        tmem_st16(ts + 16u * c, pk);
+                        l += (l0 + l1) + (l2 + l3);
+                        tmem_st_wait();
                     }
-                    l += l0 + l1;
-                    tmem_st_wait();
+                    if (!I8 && valid < kPaStep && valid % 16 != 0) {
+                        // values behind the last position that anything sees, in the last 16 that the product reads: zeros
+                        // (probability zero times whatever the page holds there would not be)
+                        const uint32_t n = 2 * tile + 1;
+                        const int st = (int)(n % NS);
+                        ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (n / NS) & 1u));
+                        if (!ok) break;
+                        const int rows = 16 - valid % 16;
+                        uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes + (h * kPaStep + valid) * 128;
+                        for (int e = quad * 32 + lane; e < rows * 8 * C::kHalves; e += 128)
+                            *reinterpret_cast<uint4*>(vt + e / (rows * 8) * C::kHalfBytes + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(prob_bar(w, step));
                 }
-                if (!I8 && mine && valid < kPaTile && valid % 16 != 0) {
-                    // values behind the last position that anything sees, in the last 16 that the product reads: zeros
-                    // (probability zero times whatever the page holds there would not be)
-                    const uint32_t n = 2 * tile + 1;
-                    const int st = (int)(n % NS);
-                    ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (n / NS) & 1u));
-                    if (!ok) break;
-                    const int rows = 16 - valid % 16;
-                    uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes + valid * 128;
-                    for (int e = quad * 32 + lane; e < rows * 8 * C::kHalves; e += 128)
-                        *reinterpret_cast<uint4*>(vt + e / (rows * 8) * C::kHalfBytes + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (I8) mbar_arrive(sempty_bar((int)(tile % C::kSteps)));
-                    if (mine) mbar_arrive(prob_bar(w));
+                if (!ok) break;
+                if constexpr (I8) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty_bar((int)(tile % C::kSteps)));
                 }
             }
             if (!ok) break;
             // ---- the rows' results over [t0, t1) ----
-            const int mine_tiles = pair ? max(t_end - t0, 0) : (t1 - t0 + 1 - w) / 2;
-            if (mine_tiles > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(odone_bar(w), done & 1u));
+            const bool some = step != step0;
+            if (some) {
+                ok = __all_sync(0xffffffffu, mbar_wait(pv_bar(w, step - 1), ((step - 1) >> 1) & 1u));
                 if (!ok) break;
-                ++done;
                 tc_fence_after();
             }
             const bool whole = t0 == 0 && t1 == item->nt;
-            const bool merge = !pair && t1 - t0 > 1;
+            const bool merge = !pair && t1 > t0 && min(2 * t1, (end + kPaStep - 1) / kPaStep) > 2 * t0 + 1;  // both have steps
             float f0 = 1.0f, f1 = 0.0f;
             if (merge && w == 1) {
                 ml[row] = make_float2(m, l);
@@ -1059,11 +1018,11 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
 #pragma unroll
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o[32];
-                    if (mine_tiles > 0) {
-                        tmem_ld32(to + c, o);
+                    if (some) {
+                        tmem_ld32(to_o + c, o);
                         if (merge) {
                             uint32_t o1[32];
-                            tmem_ld32(to + 128u + c, o1);
+                            tmem_ld32(to_o + 128u + c, o1);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e]) * f0));

@@ -112,9 +112,8 @@ def attention_error_bound(want, absv, mag, seen, d):
     int8 row's step) and the subtraction of the maximum -- (d + 8) 2^-23 mag
     absolute, the same in the maximum, so a probability is off by the factor
     exp(2 (d + 8) 2^-23 mag), and so is their sum: 4 (d + 8) 2^-23 mag sum p|v|.
-    exp2: 2^-18.4 at most (a polynomial of degree four), in a probability and in
-    the sum of them, together 2^-17; the running sums: seen 2^-22."""
-    rel = 2.0 ** -8 + 2.0 ** -17 + seen * 2.0 ** -22 + 4 * (d + 8) * 2.0 ** -23 * mag
+    exp2 and the running sums: 2^-20 + seen 2^-22."""
+    rel = 2.0 ** -8 + 2.0 ** -20 + seen * 2.0 ** -22 + 4 * (d + 8) * 2.0 ** -23 * mag
     return 2.0 ** -8 * np.abs(want) + rel[..., None] * absv + 2.0 ** -126
 
 

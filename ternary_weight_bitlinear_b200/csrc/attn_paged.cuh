@@ -397,6 +397,15 @@ __device__ __forceinline__ uint64_t pa_desc_v(uint32_t addr, int half_bytes) {
            ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A value that every lane of the warp has, in a form that the compiler knows to be one.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // 32 consecutive columns of this thread's lane (no wait).
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
     asm volatile(
@@ -523,7 +532,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     int64_t* warp_sums = plan + 8;                                      // 16 words
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan + 24);
     KvSeq* seq = reinterpret_cast<KvSeq*>(plan + 26);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = (uint32_t)uniform((int)*tmem_slot);
     // columns: scores (and probabilities) of group w's step j at 128 w + 64 (j & 1), its output at 256 + 128 w
     pdl_wait();
     pdl_launch_dependents();
@@ -685,69 +694,81 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         // ---------------- MMA issuers: warp 1 + w for softmax group w ----------------
         // Two steps of a group are in flight: while its softmax works on one, the next one's scores are made in the other
         // buffer, and the last one's probabilities are multiplied with the values.
+        // The whole warp runs this, one lane issues: what the instructions take is then uniform, and an instruction's
+        // issue is hidden behind the one before it (from a lane's own branch it took up to 195 cycles, against 48 to 64
+        // of the tensor core's).
         const int w = warp - 1;
-        if (lane == 0) {
-            const uint32_t sc = tmem + 128u * w, oc = tmem + 256u + 128u * w;
-            uint32_t n = 0;               // ring fills passed
-            uint32_t made = 0, used = 0;  // steps whose scores (whose product with the values) are issued
-            uint32_t info[2] = {0, 0};    // of the steps between the two (see below)
-            // Every group takes every fill of the rings in order, used or not: a phase's parity tells it from the ones
-            // beside it alone.
-            auto skip = [&]() {
-                const int st = (int)(n % NS);
-                if (!mbar_wait(full_bar(st), (n / NS) & 1u)) return false;
-                mbar_arrive(empty_bar(st));
-                ++n;
-                return true;
-            };
-            auto finish = [&]() {  // O (+)= P V of step `used`
-                const uint32_t x = used & 1 ? info[1] : info[0];
-                const int st = (int)(x & 0xFF), half = (int)(x >> 8) & 1, ksteps = (int)(x >> 12);
-                if (!mbar_wait(full_bar(st), (x >> 9) & 1u) || !mbar_wait(prob_bar(w, used), (used >> 1) & 1u)) return false;
-                tc_fence_after();
-                const uint64_t vd = pa_desc_v(base + C::kOffRing + st * C::kTileBytes + half * (kPaStep * 128), C::kHalfBytes);
-                const uint32_t p = sc + 64u * (used & 1);
-                for (int k = 0; k < ksteps; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
-                    tc_mma_f16_ts(oc, p + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), !((x >> 10) & 1u) || k != 0);
+        const uint32_t sc = tmem + 128u * w, oc = tmem + 256u + 128u * w;
+        uint32_t n = 0;               // ring fills passed
+        uint32_t made = 0, used = 0;  // steps whose scores (whose product with the values) are issued
+        uint32_t info0 = 0, info1 = 0;  // of the steps between the two, by parity (see below)
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, parity));
+            return ok;
+        };
+        // Every group takes every fill of the rings in order, used or not: a phase's parity tells it from the ones
+        // beside it alone.
+        auto skip = [&]() {
+            const int st = (int)(n % NS);
+            if (!wait(full_bar(st), (n / NS) & 1u)) return;
+            if (elect_one()) mbar_arrive(empty_bar(st));
+            __syncwarp();
+            ++n;
+        };
+        auto finish = [&]() {  // O (+)= P V of step `used`
+            const uint32_t x = used & 1 ? info1 : info0;
+            const int st = (int)(x & 0xFF), half = (int)(x >> 8) & 1, ksteps = (int)(x >> 12);
+            if (!wait(full_bar(st), (x >> 9) & 1u) || !wait(prob_bar(w, used), (used >> 1) & 1u)) return;
+            tc_fence_after();
+            const uint64_t vd = pa_desc_v(base + C::kOffRing + st * C::kTileBytes + half * (kPaStep * 128), C::kHalfBytes);
+            const uint32_t p = sc + 64u * (used & 1), add = (x >> 10) & 1u ? 0u : 1u;
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < kPaStep / 16; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
+                    if (k < ksteps) tc_mma_f16_ts(oc, p + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), k ? 1u : add);
                 tc_commit(pv_bar(w, used));
                 if ((x >> 11) & 1u) tc_commit(empty_bar(st));
-                ++used;
-                return true;
-            };
-            while (ok) {
-                ok = mbar_wait(ifull_bar(ii), (ii / kPaItems) & 1u);
-                if (!ok || ring[ii % kPaItems].b < 0) break;
-                const PaItem& it = ring[ii % kPaItems];
-                const bool pair = it.nsub == 2;
-                const int t0 = it.t0, t1 = it.t1, end = pair && w == 0 ? it.end0 : it.end, nq = it.nq;
-                const uint32_t slot = it.slot;
-                mbar_arrive(iempty_bar(ii));
-                ++ii;
-                // this group's Q tile (a single item's one is both groups')
-                const uint32_t own = slot + (nq == 2 ? w : 0);
-                const int from = 2 * t0 + (pair ? 0 : w), to = min(2 * t1, (end + kPaStep - 1) / kPaStep);  // its steps
-                for (int x = 0; ok && x < nq; ++x) {
-                    const uint32_t q = slot + x;
-                    ok = mbar_wait(qfull_bar((int)(q & 1)), (q >> 1) & 1u);
-                    if (ok && (q != own || from >= to)) mbar_arrive(qempty_bar((int)(q & 1)));
+            }
+            __syncwarp();
+            ++used;
+        };
+        while (ok) {
+            if (!wait(ifull_bar(ii), (ii / kPaItems) & 1u)) break;
+            const PaItem& it = ring[ii % kPaItems];
+            if (uniform(it.b) < 0) break;
+            const bool pair = uniform(it.nsub) == 2;
+            const int t0 = uniform(it.t0), t1 = uniform(it.t1), nq = uniform(it.nq);
+            const int end = uniform(pair && w == 0 ? it.end0 : it.end);
+            const uint32_t slot = (uint32_t)uniform(it.slot);
+            release();
+            // this group's Q tile (a single item's one is both groups')
+            const uint32_t own = slot + (nq == 2 ? w : 0);
+            const int from = 2 * t0 + (pair ? 0 : w), to = min(2 * t1, (end + kPaStep - 1) / kPaStep);  // its steps
+            for (int x = 0; ok && x < nq; ++x) {
+                const uint32_t q = slot + x;
+                if (wait(qfull_bar((int)(q & 1)), (q >> 1) & 1u) && (q != own || from >= to) && elect_one())
+                    mbar_arrive(qempty_bar((int)(q & 1)));
+                __syncwarp();
+            }
+            const uint64_t qd = smem_desc_sw128(base + (own & 1) * C::kTileBytes);
+            for (int t = t0; ok && t < t1; ++t) {
+                const int h0 = pair ? 0 : w, h1 = min(pair ? 2 : w + 1, to - 2 * t);  // its halves of the tile
+                if (h0 >= h1) {
+                    while (ok && used != made) finish();
+                    if (ok) skip();
+                    if (ok) skip();
+                    continue;
                 }
-                const uint64_t qd = smem_desc_sw128(base + (own & 1) * C::kTileBytes);
-                for (int t = t0; ok && t < t1; ++t) {
-                    const int h0 = pair ? 0 : w, h1 = min(pair ? 2 : w + 1, to - 2 * t);  // its halves of the tile
-                    if (h0 >= h1) {
-                        while (ok && used != made) ok = finish();
-                        ok = ok && skip() && skip();
-                        continue;
-                    }
-                    const int st = (int)(n % NS), vst = (int)((n + 1) % NS);
-                    const uint32_t ph = (n / NS) & 1u, vph = ((n + 1) / NS) & 1u;
-                    n += 2;
-                    for (int h = h0; h < h1; ++h) {
-                        if (made - used == 2 && !(ok = finish())) break;
-                        if (h == h0 && !(ok = mbar_wait(full_bar(st), ph))) break;
-                        tc_fence_after();
-                        const uint64_t kd = smem_desc_sw128(base + C::kOffRing + st * C::kTileBytes + h * (kPaStep * 128));
-                        const uint32_t s64 = sc + 64u * (made & 1);
+                const int st = (int)(n % NS), vst = (int)((n + 1) % NS);
+                const uint32_t ph = (n / NS) & 1u, vph = ((n + 1) / NS) & 1u;
+                n += 2;
+                for (int h = h0; h < h1; ++h) {
+                    if (made - used == 2) finish();
+                    if (!ok || (h == h0 && !wait(full_bar(st), ph))) break;
+                    tc_fence_after();
+                    const uint64_t kd = smem_desc_sw128(base + C::kOffRing + st * C::kTileBytes + h * (kPaStep * 128));
+                    const uint32_t s64 = sc + 64u * (made & 1);
+                    if (elect_one()) {
 #pragma unroll
                         for (int c = 0; c < C::kHalves; ++c)
 #pragma unroll
@@ -758,18 +779,22 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                         tc_commit(score_bar(w, made));
                         if (h == h1 - 1) tc_commit(empty_bar(st));
                         if (2 * t + h + (pair ? 1 : 2) >= to) tc_commit(qempty_bar((int)(own & 1)));
-                        const int valid = min(kPaStep, end - (2 * t + h) * kPaStep);
-                        const uint32_t x = (uint32_t)vst | (uint32_t)h << 8 | vph << 9 | (2 * t + h == from ? 1u << 10 : 0u) |
-                                           (h == h1 - 1 ? 1u << 11 : 0u) | (uint32_t)((valid + 15) / 16) << 12;
-                        if (made & 1) info[1] = x; else info[0] = x;
-                        ++made;
                     }
+                    __syncwarp();
+                    const int valid = min(kPaStep, end - (2 * t + h) * kPaStep);
+                    // ring place, half, its phase, first step of the item, last of the tile, products of 16 positions
+                    const uint32_t x = (uint32_t)vst | (uint32_t)h << 8 | vph << 9 | (2 * t + h == from ? 1u << 10 : 0u) |
+                                       (h == h1 - 1 ? 1u << 11 : 0u) | (uint32_t)((valid + 15) / 16) << 12;
+                    if (made & 1) info1 = x; else info0 = x;
+                    ++made;
                 }
-                // the item's last products with the values: the group's next step may be items away, and need the ring
-                // place these hold
-                while (ok && used != made) ok = finish();
             }
-            // every MMA this thread issued has finished before TMEM is freed
+            // the item's last products with the values: the group's next step may be items away, and need the ring
+            // place these hold
+            while (ok && used != made) finish();
+        }
+        // every MMA this warp issued has finished before TMEM is freed (elect.sync names the same lane every time)
+        if (elect_one()) {
             tc_commit(drain_bar(w));
             mbar_wait(drain_bar(w), 0);
         }

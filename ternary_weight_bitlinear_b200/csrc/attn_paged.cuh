@@ -1139,74 +1139,96 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
 
 // ---- merging the parts of items cut by shares ----------------------------------
 // CTA (c, y): the item that began in CTA c of the attention kernel and did not
-// end there, rows y, y + gridDim.y, ... by warp: its parts lie in CTA c and
-// the following ones up to the first that ends it, merged in that order,
+// end there, kPaMergeRows of its rows by each warp at once.  Its parts lie in
+// CTA c and the following ones up to the first that ends it, merged in that
+// order,
 //   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
+// Bound by the latency of its loads (an item has two or three parts): a warp
+// has those of its rows' next two parts on their way at once.
 constexpr int kPaMergeThreads = 128;
+constexpr int kPaMergeRows = 4;
+constexpr int kPaMergeY = 2 * kPaRows / (kPaMergeThreads / 32 * kPaMergeRows);
 
 template <int D>
-__global__ void __launch_bounds__(kPaMergeThreads) attn_merge_kernel(const PagedAttnArgs a, int grid) {
-    constexpr int DL = D / 32;
+__global__ void __launch_bounds__(kPaMergeThreads) attn_merge_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
+    constexpr int DL = D / 32, R = kPaMergeRows;
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_launch_dependents();
     const int4 it = __ldcg(a.desc + 2 * c + 1);
-    if (it.x == 0) return;
     const int nsub = it.x > a.tokens ? 2 : 1;
     const int rows0 = min(it.x, a.tokens) * a.group, rows1 = (it.x - min(it.x, a.tokens)) * a.group;
-    // the last CTA with a part of the item
-    int last = grid - 1;
-    for (int x = c + 1; x < grid; x += 32) {
-        const bool ends = x + lane < grid && __ldcg(&a.desc[2 * (x + lane)].x) == 2;
-        const uint32_t hit = __ballot_sync(0xffffffffu, ends);
-        if (hit) {
-            last = x + __ffs(hit) - 1;
-            break;
-        }
+    const int first = (blockIdx.y * (kPaMergeThreads / 32) + warp) * R;
+    if (first >= rows0 + rows1) return;  // (it.x is 0 where no item began and went on)
+    // this warp's rows of a part, and where they go
+    int at[R], tok[R], hh[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int r = min(first + i, rows0 + rows1 - 1), sub = r < rows0 ? 0 : 1, rr = sub ? r - rows0 : r;
+        at[i] = (nsub == 2 ? sub * kPaRows : 0) + rr;
+        tok[i] = sub * a.tokens + a.by_group.div(rr);
+        hh[i] = a.by_group.mod(rr);
     }
-    for (int r = blockIdx.y * (kPaMergeThreads / 32) + warp; r < rows0 + rows1; r += gridDim.y * (kPaMergeThreads / 32)) {
-        const int sub = r < rows0 ? 0 : 1, rr = sub ? r - rows0 : r;
-        const int64_t prow = (nsub == 2 ? sub * kPaRows : 0) + rr;
-        const int tok = sub * a.tokens + rr / a.group, hh = rr % a.group;
-        auto part_of = [&](int x) { return ((int64_t)x * 2 + (x == c ? 1 : 0)) * a.part_rows + prow; };
-        auto present = [&](int x) { return x <= last && (x == c || __ldcg(&a.desc[2 * x].x) != 0); };
-        float mx = -INFINITY;
-        for (int x = c; x <= last; x += 32)
-            if (present(x + lane)) mx = fmaxf(mx, __ldcg(a.part_ml + part_of(x + lane) * 2));
-        mx = warp_max_f(mx);
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        float den = 0.0f, num[DL] = {};
-        for (int x0 = c; x0 <= last; x0 += 32) {
-            float f = 0.0f, fl = 0.0f;
-            if (present(x0 + lane)) {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_ml + part_of(x0 + lane) * 2));
-                f = v.x == mx && mx != -INFINITY ? 1.0f : exp2f(v.x - ref);
-                fl = f * v.y;
+    float mx[R], den[R], num[R][DL];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        mx[i] = -INFINITY;
+        den[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < DL; ++e) num[i][e] = 0.0f;
+    }
+    for (int x0 = c; x0 < grid; x0 += 32) {
+        // states of CTAs x0 .. x0 + 31: which hold a part, and the first that ends the item
+        const int state = x0 + lane >= grid ? 0 : x0 + lane == c ? 1 : __ldcg(&a.desc[2 * (x0 + lane)].x);
+        const uint32_t ends = __ballot_sync(0xffffffffu, state == 2);
+        uint32_t some = __ballot_sync(0xffffffffu, state != 0);
+        if (ends) some &= (ends & (0u - ends)) * 2 - 1;  // up to and with the first end
+        while (some) {  // two parts at a time
+            const int p0 = __ffs(some) - 1;
+            some &= some - 1;
+            const int p1 = some ? __ffs(some) - 1 : -1;
+            some &= some - 1;
+            float v[2][R][DL];
+            float2 ml[2][R];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int x = x0 + (p == 0 || p1 < 0 ? p0 : p1);
+                const int64_t base = ((int64_t)x * 2 + (x == c ? 1 : 0)) * a.part_rows;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    ml[p][i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (base + at[i]) * 2));
+                    const float* src = a.part + (base + at[i]) * D + lane * DL;
+                    if constexpr (DL == 4)
+                        *reinterpret_cast<float4*>(v[p][i]) = __ldcg(reinterpret_cast<const float4*>(src));
+                    else
+                        *reinterpret_cast<float2*>(v[p][i]) = __ldcg(reinterpret_cast<const float2*>(src));
+                }
             }
-            const uint32_t some = __ballot_sync(0xffffffffu, present(x0 + lane));
-            den += warp_sum_f(fl);
-#pragma unroll 8
-            for (int i = 0; i < 32; ++i) {
-                if (!((some >> i) & 1)) continue;
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                const float* src = a.part + part_of(x0 + i) * D + lane * DL;
-                if constexpr (DL == 4) {
-                    const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
-                    num[0] = fmaf(fi, o.x, num[0]);
-                    num[1] = fmaf(fi, o.y, num[1]);
-                    num[2] = fmaf(fi, o.z, num[2]);
-                    num[3] = fmaf(fi, o.w, num[3]);
-                } else {
-                    const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
-                    num[0] = fmaf(fi, o.x, num[0]);
-                    num[1] = fmaf(fi, o.y, num[1]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                if (p == 1 && p1 < 0) break;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float mn = fmaxf(mx[i], ml[p][i].x);
+                    const float keep = mx[i] == -INFINITY ? 0.0f : exp2f(mx[i] - mn);
+                    const float f = ml[p][i].x == -INFINITY ? 0.0f : exp2f(ml[p][i].x - mn);
+                    den[i] = fmaf(den[i], keep, f * ml[p][i].y);
+#pragma unroll
+                    for (int e = 0; e < DL; ++e) num[i][e] = fmaf(f, v[p][i][e], num[i][e] * keep);
+                    mx[i] = mn;
                 }
             }
         }
-        const int vend = a.causal ? it.w + tok : it.w;
-        uint16_t* dst = a.out + (int64_t)(it.y + tok) * a.o_stride + (int64_t)(it.z * a.group + hh) * D + lane * DL;
+        if (ends) break;
+    }
 #pragma unroll
-        for (int e = 0; e < DL; ++e) dst[e] = float_to_bf16_bits(vend > 0 ? num[e] / den : 0.0f);
+    for (int i = 0; i < R; ++i) {
+        if (first + i >= rows0 + rows1) break;
+        const int vend = a.causal ? it.w + tok[i] : it.w;
+        uint16_t* dst = a.out + (int64_t)(it.y + tok[i]) * a.o_stride + (int64_t)(it.z * a.group + hh[i]) * D + lane * DL;
+#pragma unroll
+        for (int e = 0; e < DL; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = vend > 0 ? pack_bf16x2(num[i][e] / den[i], num[i][e + 1] / den[i]) : 0u;
     }
 }
 

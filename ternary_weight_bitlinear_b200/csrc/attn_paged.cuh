@@ -428,6 +428,26 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Eight 16-byte pieces of a lane's row exchanged among eight lanes: afterwards
+// x[i] is piece (lane & 7) of the row of lane (lane & ~7) + i, so that storing
+// x[i] writes whole 128-byte lines of four rows (a lane storing its own row's
+// pieces writes 32 half sectors).
+__device__ __forceinline__ void transpose8(uint4 (&x)[8], int lane) {
+#pragma unroll
+    for (int s = 1; s < 8; s *= 2) {
+        const bool up = lane & s;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (i & s) continue;
+            uint4& a = x[i];
+            uint4& b = x[i + s];
+            const uint4 y = make_uint4(__shfl_xor_sync(0xffffffffu, up ? a.x : b.x, s), __shfl_xor_sync(0xffffffffu, up ? a.y : b.y, s),
+                                       __shfl_xor_sync(0xffffffffu, up ? a.z : b.z, s), __shfl_xor_sync(0xffffffffu, up ? a.w : b.w, s));
+            if (up) a = y; else b = y;
+        }
+    }
+}
+
 // Registers moved between the warpgroups of a CTA (every warp of a group calls it).
 template <int N>
 __device__ __forceinline__ void setmaxnreg_inc() {
@@ -935,7 +955,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                             const float alpha = m == mn ? 1.0f : ex2((m - mn) * a.qscale);
                             m = mn;
                             l *= alpha;
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(to_o + c, o);
@@ -1033,16 +1053,13 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                 l = l * f0 + other.y * f1;
             }
             if ((pair || w == 0) && warp_live) {
-                const int r_item = sub * kPaRows + row;
                 const int slot = t0 == 0 ? 1 : 0;
-                const int64_t prow = ((int64_t)blockIdx.x * 2 + slot) * a.part_rows + r_item;
-                uint16_t* orow = a.out + (int64_t)(item->row + sub * a.tokens + tok) * a.o_stride +
-                                 (int64_t)(item->g * a.group + hh) * D;
+                const int64_t part0 = ((int64_t)blockIdx.x * 2 + slot) * a.part_rows + sub * kPaRows;
+                const int64_t prow = part0 + row;
                 const float inv = 1.0f / l;
                 float poison = 0.0f;
-#pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    uint32_t o[32];
+                // 32 columns of this row's output over both groups' parts
+                auto columns = [&](int c, uint32_t (&o)[32]) {
                     if (some) {
                         tmem_ld32(to_o + c, o);
                         if (merge) {
@@ -1058,22 +1075,52 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) poison = fmaf(__uint_as_float(o[e]), 0.0f, poison);
-                    if (live && whole) {
-                        uint32_t pk[16];
+                };
+                const int rows = tokens * a.group, r8 = quad * 32 + (lane & ~7);  // of the sub-tile; the exchange's first row
+                // (rolled: code that runs once an item is paid for in instruction fetches)
+                if (whole) {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 64) {
+                        uint4 x[8];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            pk[e] = vend > 0 ? pack_bf16x2(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv) : 0u;
+                        for (int y = 0; y < 2; ++y) {
+                            uint32_t o[32];
+                            columns(c + 32 * y, o);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint4*>(orow + c + 8 * e) = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
-                    } else if (live) {
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t pk[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(a.part + prow * D + c + 4 * e) =
-                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                                for (int z = 0; z < 4; ++z)
+                                    pk[z] = vend > 0 ? pack_bf16x2(__uint_as_float(o[8 * e + 2 * z]) * inv,
+                                                                   __uint_as_float(o[8 * e + 2 * z + 1]) * inv) : 0u;
+                                x[4 * y + e] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                            }
+                        }
+                        transpose8(x, lane);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = r8 + i, tk = a.by_group.div(r);
+                            if (r < rows)
+                                *reinterpret_cast<uint4*>(a.out + (int64_t)(item->row + sub * a.tokens + tk) * a.o_stride +
+                                                          (int64_t)(item->g * a.group + r - tk * a.group) * D + c + 8 * (lane & 7)) = x[i];
+                        }
                     }
-                    __syncwarp();
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        columns(c, o);
+                        uint4 x[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        transpose8(x, lane);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (r8 + i < rows)
+                                *reinterpret_cast<uint4*>(a.part + (part0 + r8 + i) * D + c + 4 * (lane & 7)) = x[i];
+                    }
                 }
+                __syncwarp();
                 if (live && !whole)
                     *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m == -INFINITY ? m : m * a.qscale, l);
                 if constexpr (!I8) {

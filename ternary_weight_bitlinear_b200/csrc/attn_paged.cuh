@@ -57,6 +57,20 @@ constexpr int kPaItemUnits = 1;  // cost of an item beside its tiles, in tiles o
 constexpr int kNoMask = 1 << 30;
 constexpr float kPaMaxGrowth = 8.0f;  // log2 growth of the maximum that a row's sums absorb
 
+// Two codes (the low bytes of t's halves; the high ones may be anything) as
+// bf16: a code in two's complement is m - 128 s (m: low 7 bits, s: sign), and
+// (128 + m) - (128 + 128 s) has exact terms and an exact difference.  The masks
+// come as kernel arguments: a logic instruction takes one constant, so (t & m) | c
+// with both written out is two instructions.
+struct PaCodes {
+    uint32_t m, s, c;  // 0x007F007F, 0x00800080, 0x43004300 (128 twice)
+    __device__ __forceinline__ uint32_t two(uint32_t t) const {
+        const uint32_t x = (t & m) | c, y = (t & s) | c;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+};
+
 struct PagedAttnArgs {
     KvCacheArgs c;
     KvBatchArgs b;
@@ -70,6 +84,7 @@ struct PagedAttnArgs {
     int causal;
     int box;             // positions of a page box: the largest power of two up to 128 dividing page_size
     float qscale;        // scale * log2(e)
+    PaCodes codes;
     // workspace
     float* part;         // [grid, 2, part_rows, D] unnormalised vectors
     float* part_ml;      // [grid, 2, part_rows, 2] maximum (log2 domain) and sum
@@ -825,6 +840,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         if constexpr (I8) {
             setmaxnreg_dec<C::kRegsConv>();
             const int th = threadIdx.x - 384;
+            const PaCodes codes = a.codes;
             uint32_t n = 0;
             while (const PaItem* item = take()) {
                 const int parts = 2 * (item->t1 - item->t0);  // K and V of each tile
@@ -851,13 +867,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                         for (int i = 0; i < 4; ++i)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                // a code c in two's complement is m - 128 s (m: low 7 bits, s: sign): as bf16,
-                                // (128 + m) - (128 + 128 s), each term and the difference exact
-                                const uint32_t t = __byte_perm(ws[i], 0, y ? 0x4342 : 0x4140);
-                                const uint32_t m = (t & 0x007F007Fu) | 0x43004300u, s = (t & 0x00800080u) | 0x43004300u;
-                                const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
-                                                                 *reinterpret_cast<const __nv_bfloat162*>(&s));
-                                o[2 * i + y] = *reinterpret_cast<const uint32_t*>(&d);
+                                o[2 * i + y] = codes.two(__byte_perm(ws[i], 0, y ? 0x4342 : 0x4140));
                             }
                         uint8_t* half = dst + (ch >> 2) * C::kHalfBytes;
                         *reinterpret_cast<uint4*>(half + sw128_offset(r, (ch & 3) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);

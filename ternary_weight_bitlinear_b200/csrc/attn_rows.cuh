@@ -211,16 +211,6 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// Two codes (the low bytes of t's halves; the high ones may be anything) as
-// bf16: a code in two's complement is m - 128 s (m: low 7 bits, s: sign), and
-// (128 + m) - (128 + 128 s) has exact terms and an exact difference.
-__device__ __forceinline__ uint32_t codes2(uint32_t t) {
-    const uint32_t m = (t & 0x007F007Fu) | 0x43004300u, s = (t & 0x00800080u) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&m),
-                                     *reinterpret_cast<const __nv_bfloat162*>(&s));
-    return *reinterpret_cast<const uint32_t*>(&d);
-}
-
 // The position that slot j of a product's eight stands for.  int8 rows of 128
 // bytes (in the 128-byte swizzle) are read 16 bytes a lane by slots 2k and
 // 2k + 1 together for the keys, and by the even or the odd slots together for
@@ -401,6 +391,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
         // so eight rows are a whole product.  In a result this lane holds rows 8 x + 2 kq and 8 x + 2 kq + 1 at position
         // (dimension) slots r8 and r8 + 8.
         constexpr int X = NR / 8;
+        const PaCodes codes = a.codes;
         const int w = ct >> 5, r8 = lane >> 2, kq = lane & 3;
         float* osm = reinterpret_cast<float*>(sm + C::kOffO);
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
@@ -495,8 +486,8 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                                 const uint4 &u = y[2 * pb], &v = y[2 * pb + 1];
                                 const uint32_t u1 = k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
                                 const uint32_t v1 = k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w;
-                                const uint32_t ak[4] = {codes2(__byte_perm(u1, 0, 0x4140)), codes2(__byte_perm(v1, 0, 0x4140)),
-                                                        codes2(__byte_perm(u1, 0, 0x4342)), codes2(__byte_perm(v1, 0, 0x4342))};
+                                const uint32_t ak[4] = {codes.two(__byte_perm(u1, 0, 0x4140)), codes.two(__byte_perm(v1, 0, 0x4140)),
+                                                        codes.two(__byte_perm(u1, 0, 0x4342)), codes.two(__byte_perm(v1, 0, 0x4342))};
 #pragma unroll
                                 for (int x = 0; x < X; ++x) mma_bf16(s[pb][x], ak, q[4 * blk + k][x][0], q[4 * blk + k][x][1]);
                             }
@@ -611,7 +602,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                             for (int y = 0; y < 4; ++y) {
                                 const int b = 2 * db + (y & 1);
                                 const uint32_t pick = (uint32_t)((b & 3) | ((4 + (b & 3)) << 8));  // its bytes 0 and 2
-                                av[y] = codes2(__byte_perm(v[2 * (y >> 1)][b >> 2], v[2 * (y >> 1) + 1][b >> 2], pick));
+                                av[y] = codes.two(__byte_perm(v[2 * (y >> 1)][b >> 2], v[2 * (y >> 1) + 1][b >> 2], pick));
                             }
 #pragma unroll
                             for (int x = 0; x < X; ++x) mma_bf16(o[db][x], av, p[pb][x][0], p[pb][x][1]);

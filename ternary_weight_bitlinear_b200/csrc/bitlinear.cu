@@ -1496,6 +1496,7 @@ bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batc
     a.by_group = fast_div(a.group);
     a.causal = causal != 0;
     a.qscale = scale * kLog2e;
+    a.codes = {0x007F007Fu, 0x00800080u, 0x43004300u};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto run = cache->head_dim == 128
                    ? (cache->format == BL_KV_I8 ? attn_paged_launch<128, true> : attn_paged_launch<128, false>)

@@ -105,13 +105,13 @@ class KvCache(ctypes.Structure):
     _fields_ = [("k", _P), ("v", _P), ("k_step", _P), ("v_step", _P), ("num_pages", _I64), ("page_size", _I64),
                 ("kv_heads", _I64), ("head_dim", _I64), ("stride_page", _I64), ("stride_slot", _I64),
                 ("stride_head", _I64), ("format", _INT)]
-    shape = device = None  # (kv_heads, head_dim) and the tensors' device, from make_kv_cache
+    facts = None  # (kv_heads, head_dim, device), from make_kv_cache
 
 
 class KvBatch(ctypes.Structure):
     """bl_kv_batch: the sequences of one step (see make_kv_batch)."""
     _fields_ = [("cu_q", _P), ("kv_len", _P), ("pages", _P), ("batch", _I64), ("max_pages", _I64)]
-    device = None
+    device = None  # from make_kv_batch
 
 
 class BitLinearError(RuntimeError):
@@ -397,48 +397,50 @@ def bitlinear_attn_decode(q, k_cache, v_cache, L, q_heads, kv_heads, scale, out=
 
 
 # --- paged key/value cache --------------------------------------------------------
-# (Called once a layer and token: the marshalling is kept short.)
+# (Called once a layer and token: each attribute of a tensor is asked for once.)
 def make_kv_cache(k_pages, v_pages, k_step=None, v_step=None):
     """A bl_kv_cache of k_pages, v_pages [num_pages, page_size, kv_heads, head_dim]
     (any strides, the same for both, head_dim contiguous), bf16, or int8 with
     fp32 steps k_step, v_step [num_pages, kv_heads, page_size].  Holds its tensors."""
-    dtype = k_pages.dtype
-    i8 = dtype == torch.int8
-    strides, shape, dev = k_pages.stride(), k_pages.shape, k_pages.device
-    if not (k_pages.is_cuda and len(shape) == 4 and (i8 or dtype == torch.bfloat16)):
+    dtype, strides, shape, dev = k_pages.dtype, k_pages.stride(), k_pages.shape, k_pages.get_device()
+    i8 = dtype is torch.int8
+    if dev < 0 or len(shape) != 4 or not (i8 or dtype is torch.bfloat16):
         raise TypeError("k_pages and v_pages must be CUDA tensors of four dimensions, both bfloat16 or both int8")
-    if v_pages.dtype != dtype or v_pages.device != dev or v_pages.shape != shape or v_pages.stride() != strides \
-            or strides[3] != 1:
+    if v_pages.dtype is not dtype or v_pages.get_device() != dev or v_pages.shape != shape \
+            or v_pages.stride() != strides or strides[3] != 1:
         raise TypeError("k_pages and v_pages must have the same type, device, shape and strides, with head_dim contiguous")
     n, page, heads, d = shape
+    ks = vs = None
     if i8:
         for t in (k_step, v_step):
-            if _need(t, torch.float32, "the steps of an int8 cache", 3).shape != (n, heads, page) or t.device != dev:
-                raise TypeError("k_step and v_step must be [num_pages, kv_heads, page_size], on the pages' device")
+            if t is None or t.dtype is not torch.float32 or not t.is_contiguous() or t.shape != (n, heads, page) \
+                    or t.get_device() != dev:
+                raise TypeError("k_step and v_step must be contiguous torch.float32 tensors [num_pages, kv_heads, "
+                                "page_size] on the pages' device")
+        ks, vs = k_step.data_ptr(), v_step.data_ptr()
     elif k_step is not None or v_step is not None:
         raise TypeError("a bfloat16 cache has no steps")
-    c = KvCache(k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_step), _addr(v_step), n, page, heads, d,
-                strides[0], strides[1], strides[2], BL_KV_I8 if i8 else BL_KV_BF16)
-    c.tensors = (k_pages, v_pages, k_step, v_step)
-    c.device = dev
-    c.shape = (heads, d)
+    c = KvCache(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, n, page, heads, d, strides[0], strides[1], strides[2],
+                BL_KV_I8 if i8 else BL_KV_BF16)
+    c.held = (k_pages, v_pages, k_step, v_step)
+    c.facts = (heads, d, dev)
     return c
 
 
 def make_kv_batch(cu_q, kv_len, pages):
     """A bl_kv_batch of int32 CUDA tensors cu_q [batch + 1], kv_len [batch] and
     pages [batch, max_pages].  Holds its tensors; the kernels read their contents."""
-    _need(cu_q, torch.int32, "cu_q", 1)
-    _need(kv_len, torch.int32, "kv_len", 1)
-    _need(pages, torch.int32, "pages", 2)
-    batch, max_pages = pages.shape
-    dev = pages.device
-    if cu_q.shape[0] != batch + 1 or kv_len.shape[0] != batch:
+    i32, dev, shape = torch.int32, pages.get_device(), pages.shape
+    if dev < 0 or cu_q.get_device() != dev or kv_len.get_device() != dev:
+        raise TypeError("cu_q, kv_len and pages must be CUDA tensors on one device")
+    if len(shape) != 2 or cu_q.dtype is not i32 or kv_len.dtype is not i32 or pages.dtype is not i32 \
+            or not (cu_q.is_contiguous() and kv_len.is_contiguous() and pages.is_contiguous()):
+        raise TypeError("cu_q, kv_len and pages must be contiguous torch.int32 tensors, pages of two dimensions")
+    batch, max_pages = shape
+    if cu_q.shape != (batch + 1,) or kv_len.shape != (batch,):
         raise TypeError("cu_q must have batch + 1 entries, kv_len batch and pages batch rows")
-    if cu_q.device != dev or kv_len.device != dev:
-        raise TypeError("cu_q, kv_len and pages must be on one device")
     b = KvBatch(cu_q.data_ptr(), kv_len.data_ptr(), pages.data_ptr(), batch, max_pages)
-    b.tensors = (cu_q, kv_len, pages)
+    b.held = (cu_q, kv_len, pages)
     b.device = dev
     return b
 
@@ -447,13 +449,24 @@ def _kv_rows(t, d, name, dev):
     """(rows, heads, elements between rows) of bf16 rows [T, heads, head_dim] or
     [T, heads * head_dim], heads contiguous, rows with any stride."""
     n = t.shape
-    if t.dtype != torch.bfloat16 or t.device != dev or not 2 <= len(n) <= 3:
+    dims = len(n)
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or dims < 2 or dims > 3:
         raise TypeError("%s must be a torch.bfloat16 tensor of two or three dimensions, on the cache's device" % name)
     s = t.stride()
-    width = n[1] if len(n) == 2 else n[1] * n[2]
-    if s[-1] != 1 or width % d or (len(n) == 3 and (n[2] != d or (n[1] > 1 and s[1] != d))):
-        raise TypeError("%s must have rows of contiguous heads of %d" % (name, d))
-    return n[0], width // d, (s[0] if n[0] > 1 else width)
+    if dims == 3:
+        rows, heads, width = n
+        if s[2] == 1 and width == d and (s[1] == d or heads == 1):
+            return rows, heads, s[0] if rows > 1 else heads * d
+    elif s[1] == 1 and n[1] % d == 0:
+        return n[0], n[1] // d, s[0] if n[0] > 1 else n[1]
+    raise TypeError("%s must have rows of contiguous heads of %d" % (name, d))
+
+
+def _kv_facts(cache, batch):
+    """(kv_heads, head_dim, device) of a cache, which the batch has to be on too."""
+    if cache.facts is None or batch.device != cache.facts[2]:
+        raise TypeError("the cache and the batch must come from make_kv_cache and make_kv_batch, on one device")
+    return cache.facts
 
 
 def _kv_new(make, stream):
@@ -464,19 +477,17 @@ def _kv_new(make, stream):
         return make()
 
 
-def _kv_call(fn, cache, batch, stream, *args):
+def _kv_call(fn, dev, stream, cache, batch, *args):
     """The entry point `fn` on the stream (None: the device's current one), with
     the cache's device current, as the library needs it."""
-    dev = cache.device
-    if batch.device != dev:
-        raise TypeError("the cache and the batch must be on one device")
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
-        status = getattr(lib(), fn)(ctypes.byref(cache), ctypes.byref(batch), *args, raw)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    call = getattr(_lib or lib(), fn)
+    if dev == torch._C._cuda_getDevice():
+        status = call(ctypes.byref(cache), ctypes.byref(batch), *args, raw)
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), fn)(ctypes.byref(cache), ctypes.byref(batch), *args, raw)
-    if status != 0:
+            status = call(ctypes.byref(cache), ctypes.byref(batch), *args, raw)
+    if status:
         raise BitLinearError(fn, status)
 
 
@@ -484,19 +495,19 @@ def bitlinear_kv_write(k, v, cache, batch, stream=None):
     """New rows k, v (bf16 [T, kv_heads, head_dim], rows with any stride) into the
     pages of a make_kv_cache() at the places of a make_kv_batch(); quantised per
     row when the cache is int8."""
-    heads, d = cache.shape
-    T, hk, sk = _kv_rows(k, d, "k", cache.device)
-    Tv, hv, sv = _kv_rows(v, d, "v", cache.device)
+    heads, d, dev = _kv_facts(cache, batch)
+    T, hk, sk = _kv_rows(k, d, "k", dev)
+    Tv, hv, sv = _kv_rows(v, d, "v", dev)
     if hk != heads or hv != heads or Tv != T:
         raise TypeError("k and v must be [T, kv_heads, head_dim]")
-    _kv_call("bitlinear_kv_write", cache, batch, stream, k.data_ptr(), sk, v.data_ptr(), sv, T)
+    _kv_call("bitlinear_kv_write", dev, stream, cache, batch, k.data_ptr(), sk, v.data_ptr(), sv, T)
 
 
 def bitlinear_kv_read(cache, batch, T=None, k=None, v=None, stream=None):
     """The rows of a batch read back out of the cache: (k, v) bf16 [T, kv_heads,
     head_dim], into the given tensors or new ones of T rows.  Rows of no sequence
     are left as they were (in a new tensor: zeros)."""
-    heads, d = cache.shape
+    heads, d, dev = _kv_facts(cache, batch)
     if k is None or v is None:
         if T is None:
             if k is None and v is None:
@@ -504,15 +515,15 @@ def bitlinear_kv_read(cache, batch, T=None, k=None, v=None, stream=None):
             T = (v if k is None else k).shape[0]
 
         def new():
-            return torch.zeros((T, heads, d), dtype=torch.bfloat16, device=cache.device)
+            return torch.zeros((T, heads, d), dtype=torch.bfloat16, device=torch.device("cuda", dev))
 
         k = _kv_new(new, stream) if k is None else k
         v = _kv_new(new, stream) if v is None else v
-    Tk, hk, sk = _kv_rows(k, d, "k", cache.device)
-    Tv, hv, sv = _kv_rows(v, d, "v", cache.device)
+    Tk, hk, sk = _kv_rows(k, d, "k", dev)
+    Tv, hv, sv = _kv_rows(v, d, "v", dev)
     if hk != heads or hv != heads or Tv != Tk or (T is not None and T != Tk):
         raise TypeError("k and v must be [T, kv_heads, head_dim]")
-    _kv_call("bitlinear_kv_read", cache, batch, stream, k.data_ptr(), sk, v.data_ptr(), sv, Tk)
+    _kv_call("bitlinear_kv_read", dev, stream, cache, batch, k.data_ptr(), sk, v.data_ptr(), sv, Tk)
     return k, v
 
 
@@ -522,7 +533,7 @@ def _attn_paged_workspace(T, q_heads, kv_heads, head_dim, device):
     with torch.cuda.device(device) if device is not None else contextlib.nullcontext():
         _check("bitlinear_attn_paged_workspace_size",
                lib().bitlinear_attn_paged_workspace_size(T, q_heads, kv_heads, head_dim, ctypes.byref(n)))
-    return n.value
+    return max(n.value, 16)
 
 
 def bitlinear_attn_paged_workspace_size(T, q_heads, kv_heads, head_dim):
@@ -536,21 +547,25 @@ def bitlinear_attn_paged(q, cache, batch, scale, causal=True, out=None, workspac
     any stride) over the paged cache, which holds their own keys and values
     already: bf16, the shape of q.  Rows of no sequence are left as they were (in
     a new tensor: zeros)."""
-    kv_heads, d = cache.shape
-    dev = cache.device
+    kv_heads, d, dev = _kv_facts(cache, batch)
     T, heads, sq = _kv_rows(q, d, "q", dev)
     if out is None:
-        out = _kv_new(lambda: torch.zeros(q.shape, dtype=torch.bfloat16, device=dev), stream)
+        out = _kv_new(lambda: q.new_zeros(q.shape), stream)
     To, ho, so = _kv_rows(out, d, "out", dev)
     if ho != heads or To != T:
         raise TypeError("out must have the shape of q")
     if workspace is None:
-        nbytes = _attn_paged_workspace(T, heads, kv_heads, d, dev.index)
-        workspace = _kv_new(lambda: torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev), stream)
-    elif workspace.device != dev:
-        raise TypeError("the workspace must be on the cache's device")
-    _kv_call("bitlinear_attn_paged", cache, batch, stream, q.data_ptr(), sq, T, heads, scale, 1 if causal else 0,
-             out.data_ptr(), so, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        nbytes = _attn_paged_workspace(T, heads, kv_heads, d, dev)
+        if stream is None:
+            workspace = q.new_empty(nbytes, dtype=torch.uint8)
+        else:
+            workspace = _kv_new(lambda: q.new_empty(nbytes, dtype=torch.uint8), stream)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise TypeError("the workspace must be contiguous, on the cache's device")
+        nbytes = workspace.numel() * workspace.element_size()
+    _kv_call("bitlinear_attn_paged", dev, stream, cache, batch, q.data_ptr(), sq, T, heads, scale, 1 if causal else 0,
+             out.data_ptr(), so, workspace.data_ptr(), nbytes)
     return out
 
 

@@ -180,7 +180,7 @@ def test_bad_pages_are_recorded(guard):
     ref = B.bitlinear_attn_paged(q, p.cache, p.batch, 0.125)
     for bad in (-1, p.kc.shape[0], 2 ** 31 - 1, -2 ** 31):
         p.pages[0, 1] = bad
-        p.batch.tensors[2].copy_(torch.from_numpy(p.pages))
+        p.batch.held[2].copy_(torch.from_numpy(p.pages))
         out = B.bitlinear_attn_paged(q, p.cache, p.batch, 0.125)
         assert B.bitlinear_device_status() == 9
         assert torch.equal(out[4:], ref[4:])  # the other sequence is not affected
@@ -191,8 +191,8 @@ def test_arrays_that_lie_stay_inside_the_buffers(guard):
     q = torch.randn((p.T, 4, 64), device="cuda").to(torch.bfloat16)
     for cu, lens in (([-5, 3, 900], [20, 20]), ([0, 4, 8], [2 ** 31 - 1, -7]), ([8, 4, 0], [20, 20]),
                      ([2 ** 31 - 1, -2 ** 31, 5], [20, 20])):
-        p.batch.tensors[0].copy_(torch.tensor(cu, dtype=torch.int32))
-        p.batch.tensors[1].copy_(torch.tensor(lens, dtype=torch.int32))
+        p.batch.held[0].copy_(torch.tensor(cu, dtype=torch.int32))
+        p.batch.held[1].copy_(torch.tensor(lens, dtype=torch.int32))
         out = guard.empty((p.T, 4, 64), torch.bfloat16)
         ws = guard.workspace(max(16, B.bitlinear_attn_paged_workspace_size(p.T, 4, 2, 64)))
         B.bitlinear_attn_paged(q, p.cache, p.batch, 0.125, out=out, workspace=ws)
@@ -216,7 +216,7 @@ def test_graphs_that_share_a_workspace(guard):
         graphs.append(g)
     for lens in (([900, 70, 2000], [700, 1500]), ([2, 70, 1999], [50, 1])):
         for p, l in zip(ps, lens):
-            p.batch.tensors[1].copy_(torch.tensor(l, dtype=torch.int32))
+            p.batch.held[1].copy_(torch.tensor(l, dtype=torch.int32))
         for o in outs:
             o.zero_()
         for _ in range(3):

@@ -135,7 +135,7 @@ def test_page_outside_the_cache_is_recorded_and_skipped(guard):
         p = Paged(guard, [20, 3], [20, 3], 16, 2, 64, fmt, seed=10, poison=False)
         for bad in (-1, p.kc.shape[0], 2 ** 31 - 1, -2 ** 31):
             p.pages[0, 1] = bad
-            p.batch.tensors[2].copy_(torch.from_numpy(p.pages))
+            p.batch.held[2].copy_(torch.from_numpy(p.pages))
             k, v, kd, vd = rows_of(p, seed=11)
             before = p.device_pages()
             B.bitlinear_kv_write(kd, vd, p.cache, p.batch)
@@ -155,8 +155,8 @@ def test_arrays_that_lie_stay_inside_the_buffers(guard):
     p = Paged(guard, [4, 4], [20, 20], 16, 2, 64, "int8", seed=12, poison=False, spare=6)
     for cu, lens in (([-5, 3, 900], [20, 20]), ([0, 4, 8], [2 ** 31 - 1, -7]), ([8, 4, 0], [20, 20]),
                      ([2 ** 31 - 1, -2 ** 31, 5], [20, 20])):
-        p.batch.tensors[0].copy_(torch.tensor(cu, dtype=torch.int32))
-        p.batch.tensors[1].copy_(torch.tensor(lens, dtype=torch.int32))
+        p.batch.held[0].copy_(torch.tensor(cu, dtype=torch.int32))
+        p.batch.held[1].copy_(torch.tensor(lens, dtype=torch.int32))
         k, v, kd, vd = rows_of(p, seed=13)
         B.bitlinear_kv_write(kd, vd, p.cache, p.batch)
         B.bitlinear_kv_read(p.cache, p.batch, T=p.T)
@@ -178,7 +178,7 @@ def test_write_on_another_stream_and_in_a_graph(guard):
     # the captured call reads the lengths and rows of the moment of its replay
     p.kc, p.vc, p.ks, p.vs = first
     p.lens = [39, 9]
-    p.batch.tensors[1].copy_(torch.tensor(p.lens, dtype=torch.int32))
+    p.batch.held[1].copy_(torch.tensor(p.lens, dtype=torch.int32))
     k2, v2, kd2, vd2 = rows_of(p, seed=16)
     kd.copy_(kd2)
     vd.copy_(vd2)

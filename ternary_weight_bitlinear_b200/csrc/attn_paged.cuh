@@ -1196,37 +1196,59 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
 
 // ---- merging the parts of items cut by shares ----------------------------------
 // CTA (c, y): the item that began in CTA c of the attention kernel and did not
-// end there, kPaMergeRows of its rows by each warp at once.  Its parts lie in
-// CTA c and the following ones up to the first that ends it, merged in that
-// order,
+// end there; kPaMergeRows of its rows by each warp.  Its parts lie in CTA c and
+// the following ones up to the first that ends it, merged in that order,
 //   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-// Bound by the latency of its loads (an item has two or three parts): a warp
-// has those of its rows' next two parts on their way at once.
+// Bound by the latency of its loads: those of the first two parts (mostly all
+// there are) go out together with those that say which CTAs hold one, the
+// others' four at a time.
 constexpr int kPaMergeThreads = 128;
-constexpr int kPaMergeRows = 4;
-constexpr int kPaMergeY = 2 * kPaRows / (kPaMergeThreads / 32 * kPaMergeRows);
+constexpr int kPaMergeRows = 2;
+constexpr int kPaMergeBlock = kPaMergeThreads / 32 * kPaMergeRows;
 
 template <int D>
 __global__ void __launch_bounds__(kPaMergeThreads) attn_merge_kernel(const __grid_constant__ PagedAttnArgs a, int grid) {
     constexpr int DL = D / 32, R = kPaMergeRows;
     const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row0 = blockIdx.y * kPaMergeBlock + warp * R;  // this warp's rows of a part
     pdl_wait();
     pdl_launch_dependents();
-    const int4 it = __ldcg(a.desc + 2 * c + 1);
-    const int nsub = it.x > a.tokens ? 2 : 1;
-    const int rows0 = min(it.x, a.tokens) * a.group, rows1 = (it.x - min(it.x, a.tokens)) * a.group;
-    const int first = (blockIdx.y * (kPaMergeThreads / 32) + warp) * R;
-    if (first >= rows0 + rows1) return;  // (it.x is 0 where no item began and went on)
-    // this warp's rows of a part, and where they go
-    int at[R], tok[R], hh[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-        const int r = min(first + i, rows0 + rows1 - 1), sub = r < rows0 ? 0 : 1, rr = sub ? r - rows0 : r;
-        at[i] = (nsub == 2 ? sub * kPaRows : 0) + rr;
-        tok[i] = sub * a.tokens + a.by_group.div(rr);
-        hh[i] = a.by_group.mod(rr);
-    }
     float mx[R], den[R], num[R][DL];
+    // N parts' loads, then their sums in order; used: bits of those that count
+    auto parts = [&](auto n_tag, const int* x, uint32_t& some, auto&& used) {
+        constexpr int N = decltype(n_tag)::value;
+        float v[N][R][DL];
+        float2 ml[N][R];
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            const int64_t base = ((int64_t)x[p] * 2 + (x[p] == c ? 1 : 0)) * a.part_rows;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int64_t at = base + min(row0 + i, a.part_rows - 1);
+                ml[p][i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + at * 2));
+                const float* src = a.part + at * D + lane * DL;
+                if constexpr (DL == 4)
+                    *reinterpret_cast<float4*>(v[p][i]) = __ldcg(reinterpret_cast<const float4*>(src));
+                else
+                    *reinterpret_cast<float2*>(v[p][i]) = __ldcg(reinterpret_cast<const float2*>(src));
+            }
+        }
+        const uint32_t count = used(some);
+#pragma unroll
+        for (int p = 0; p < N; ++p) {
+            if (!((count >> p) & 1u)) continue;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const float mn = fmaxf(mx[i], ml[p][i].x);
+                const float keep = mx[i] == -INFINITY ? 0.0f : exp2f(mx[i] - mn);
+                const float f = ml[p][i].x == -INFINITY ? 0.0f : exp2f(ml[p][i].x - mn);
+                den[i] = fmaf(den[i], keep, f * ml[p][i].y);
+#pragma unroll
+                for (int e = 0; e < DL; ++e) num[i][e] = fmaf(f, v[p][i][e], num[i][e] * keep);
+                mx[i] = mn;
+            }
+        }
+    };
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         mx[i] = -INFINITY;
@@ -1234,58 +1256,50 @@ __global__ void __launch_bounds__(kPaMergeThreads) attn_merge_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < DL; ++e) num[i][e] = 0.0f;
     }
-    for (int x0 = c; x0 < grid; x0 += 32) {
-        // states of CTAs x0 .. x0 + 31: which hold a part, and the first that ends the item
-        const int state = x0 + lane >= grid ? 0 : x0 + lane == c ? 1 : __ldcg(&a.desc[2 * (x0 + lane)].x);
-        const uint32_t ends = __ballot_sync(0xffffffffu, state == 2);
-        uint32_t some = __ballot_sync(0xffffffffu, state != 0);
-        if (ends) some &= (ends & (0u - ends)) * 2 - 1;  // up to and with the first end
-        while (some) {  // two parts at a time
-            const int p0 = __ffs(some) - 1;
-            some &= some - 1;
-            const int p1 = some ? __ffs(some) - 1 : -1;
-            some &= some - 1;
-            float v[2][R][DL];
-            float2 ml[2][R];
+    const int4 it = __ldcg(a.desc + 2 * c + 1);
+    if (it.x == 0 || (row0 >= kPaRows && it.x <= a.tokens)) return;  // no item began here and went on; no second sub-tile
+    int state = c + lane >= grid ? 0 : lane == 0 ? 1 : __ldcg(&a.desc[2 * (c + lane)].x);
+    // which of CTAs x0 .. x0 + 31 hold a part: up to and with the first that ends the item
+    uint32_t ends = 0, some = 0;
+    auto holders = [&]() {
+        ends = __ballot_sync(0xffffffffu, state == 2);
+        const uint32_t have = __ballot_sync(0xffffffffu, state != 0);
+        return ends ? have & ((ends & (0u - ends)) * 2 - 1) : have;
+    };
+    const int near[2] = {c, min(c + 1, grid - 1)};
+    parts(std::integral_constant<int, 2>{}, near, some, [&](uint32_t& left) {
+        const uint32_t all = holders();
+        left = all & ~3u;
+        return all & 3u;
+    });
+    for (int x0 = c;;) {
+        while (some) {
+            int x[4];
+            uint32_t count = 0;
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int x = x0 + (p == 0 || p1 < 0 ? p0 : p1);
-                const int64_t base = ((int64_t)x * 2 + (x == c ? 1 : 0)) * a.part_rows;
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    ml[p][i] = __ldcg(reinterpret_cast<const float2*>(a.part_ml + (base + at[i]) * 2));
-                    const float* src = a.part + (base + at[i]) * D + lane * DL;
-                    if constexpr (DL == 4)
-                        *reinterpret_cast<float4*>(v[p][i]) = __ldcg(reinterpret_cast<const float4*>(src));
-                    else
-                        *reinterpret_cast<float2*>(v[p][i]) = __ldcg(reinterpret_cast<const float2*>(src));
-                }
+            for (int p = 0; p < 4; ++p) {
+                count |= some ? 1u << p : 0u;
+                x[p] = some ? x0 + __ffs(some) - 1 : c;
+                some &= some - 1;
             }
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                if (p == 1 && p1 < 0) break;
-#pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float mn = fmaxf(mx[i], ml[p][i].x);
-                    const float keep = mx[i] == -INFINITY ? 0.0f : exp2f(mx[i] - mn);
-                    const float f = ml[p][i].x == -INFINITY ? 0.0f : exp2f(ml[p][i].x - mn);
-                    den[i] = fmaf(den[i], keep, f * ml[p][i].y);
-#pragma unroll
-                    for (int e = 0; e < DL; ++e) num[i][e] = fmaf(f, v[p][i][e], num[i][e] * keep);
-                    mx[i] = mn;
-                }
-            }
+            parts(std::integral_constant<int, 4>{}, x, some, [&](uint32_t&) { return count; });
         }
-        if (ends) break;
+        if (ends || (x0 += 32) >= grid) break;
+        state = x0 + lane >= grid ? 0 : __ldcg(&a.desc[2 * (x0 + lane)].x);
+        some = holders();
     }
+    const int rows0 = min(it.x, a.tokens) * a.group, rows1 = (it.x - min(it.x, a.tokens)) * a.group;  // of its sub-tiles
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        if (first + i >= rows0 + rows1) break;
-        const int vend = a.causal ? it.w + tok[i] : it.w;
-        uint16_t* dst = a.out + (int64_t)(it.y + tok[i]) * a.o_stride + (int64_t)(it.z * a.group + hh[i]) * D + lane * DL;
+        const int sub = (row0 + i) / kPaRows, rr = (row0 + i) % kPaRows;
+        if (rr >= (sub == 0 ? rows0 : rows1)) continue;
+        const int in_sub = a.by_group.div(rr), tok = sub * a.tokens + in_sub, hh = rr - in_sub * a.group;
+        const int vend = a.causal ? it.w + tok : it.w;
+        const float inv = 1.0f / den[i];
+        uint16_t* dst = a.out + (int64_t)(it.y + tok) * a.o_stride + (int64_t)(it.z * a.group + hh) * D + lane * DL;
 #pragma unroll
         for (int e = 0; e < DL; e += 2)
-            *reinterpret_cast<uint32_t*>(dst + e) = vend > 0 ? pack_bf16x2(num[i][e] / den[i], num[i][e + 1] / den[i]) : 0u;
+            *reinterpret_cast<uint32_t*>(dst + e) = vend > 0 ? pack_bf16x2(num[i][e] * inv, num[i][e + 1] * inv) : 0u;
     }
 }
 

@@ -965,7 +965,8 @@ bl_status attn_paged_launch(PagedAttnArgs& a, void* workspace, int dev, const De
     const bl_status st = launch(attn_paged_kernel<D, I8>, dim3((unsigned)info.sms), dim3(C::kThreads), (size_t)C::kSmem,
                                 stream, map_q, map_k, map_v, (const PagedAttnArgs&)a);
     if (st != BL_OK) return st;
-    return launch(attn_merge_kernel<D>, dim3((unsigned)info.sms, kPaMergeY), dim3(kPaMergeThreads), 0, stream,
+    return launch(attn_merge_kernel<D>, dim3((unsigned)info.sms, (unsigned)((a.part_rows + kPaMergeBlock - 1) / kPaMergeBlock)),
+                  dim3(kPaMergeThreads), 0, stream,
                   (const PagedAttnArgs&)a, info.sms);
 }
 

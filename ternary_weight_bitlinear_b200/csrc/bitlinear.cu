@@ -846,18 +846,21 @@ bl_status kv_rows_check(const void* p, int64_t stride, int64_t width) {
     return aligned16(p) && stride % 8 == 0 ? BL_OK : BL_ERR_ALIGN;
 }
 
-// Rows a group of lanes takes in turn: four keep enough loads in flight where
-// there are many rows, one spreads few over more SMs (5 heads of 128, bf16:
-// 256 rows 2.0 us by one, 3.2 by four; 2048 rows 6.9 and 4.3; 16384 rows 32 and 15).
-constexpr int kKvMany = 4;
-bool kv_many(int64_t T, int64_t kv_heads, int64_t head_dim, int sms) {
-    const int64_t groups = kKvThreads / (head_dim / 8) * kKvMany;
-    return T * kv_heads >= 2 * groups * sms;
+// Rows a group of lanes takes in turn: several keep enough loads in flight where
+// there are many rows, one spreads few over more SMs (5 heads of 128, bf16: 256
+// rows 2.0 us by one, 3.2 by four; 2048 rows 6.9 and 4.3; 16384 rows 32 and 15.
+// int8, whose lanes hold two bf16 vectors each: 16384 rows 17 by four, 14 by two).
+constexpr int kKvManyBf16 = 4, kKvManyI8 = 2;
+// Rows that a block takes when each of its groups takes one.
+int64_t kv_groups(const bl_kv_cache* c) {
+    return kKvThreads / (c->head_dim / (c->format == BL_KV_I8 ? 8 * kKvVecs<true> : 8 * kKvVecs<false>));
 }
-
-unsigned kv_grid(int64_t T, int64_t kv_heads, int64_t head_dim, int rows) {
-    const int64_t groups = kKvThreads / (head_dim / 8) * rows;
-    return (unsigned)((T * kv_heads + groups - 1) / groups);
+bool kv_many(const bl_kv_cache* c, int64_t T, int sms) {
+    return T * c->kv_heads >= 2 * (c->format == BL_KV_I8 ? kKvManyI8 : kKvManyBf16) * kv_groups(c) * sms;
+}
+unsigned kv_grid(const bl_kv_cache* c, int64_t T, int rows) {
+    const int64_t block = kv_groups(c) * rows;
+    return (unsigned)((T * c->kv_heads + block - 1) / block);
 }
 
 bl_status attn_paged_check(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim) {
@@ -1423,13 +1426,13 @@ bl_status bitlinear_kv_write(const bl_kv_cache* cache, const bl_kv_batch* batch,
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != BL_OK) return st;
     const bool i8 = cache->format == BL_KV_I8;
-    const bool many = kv_many(T, cache->kv_heads, cache->head_dim, info.sms);
+    const bool many = kv_many(cache, T, info.sms);
     auto kernel = cache->head_dim == 128
-                      ? (i8 ? (many ? kv_write_kernel<128, true, kKvMany> : kv_write_kernel<128, true, 1>)
-                            : (many ? kv_write_kernel<128, false, kKvMany> : kv_write_kernel<128, false, 1>))
-                      : (i8 ? (many ? kv_write_kernel<64, true, kKvMany> : kv_write_kernel<64, true, 1>)
-                            : (many ? kv_write_kernel<64, false, kKvMany> : kv_write_kernel<64, false, 1>));
-    return launch(kernel, dim3(kv_grid(T, cache->kv_heads, cache->head_dim, many ? kKvMany : 1)), dim3(kKvThreads), 0,
+                      ? (i8 ? (many ? kv_write_kernel<128, true, kKvManyI8> : kv_write_kernel<128, true, 1>)
+                            : (many ? kv_write_kernel<128, false, kKvManyBf16> : kv_write_kernel<128, false, 1>))
+                      : (i8 ? (many ? kv_write_kernel<64, true, kKvManyI8> : kv_write_kernel<64, true, 1>)
+                            : (many ? kv_write_kernel<64, false, kKvManyBf16> : kv_write_kernel<64, false, 1>));
+    return launch(kernel, dim3(kv_grid(cache, T, !many ? 1 : i8 ? kKvManyI8 : kKvManyBf16)), dim3(kKvThreads), 0,
                   static_cast<cudaStream_t>(stream), c, b, k, k_stride, v, v_stride);
 }
 
@@ -1447,13 +1450,13 @@ bl_status bitlinear_kv_read(const bl_kv_cache* cache, const bl_kv_batch* batch, 
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != BL_OK) return st;
     const bool i8 = cache->format == BL_KV_I8;
-    const bool many = kv_many(T, cache->kv_heads, cache->head_dim, info.sms);
+    const bool many = kv_many(cache, T, info.sms);
     auto kernel = cache->head_dim == 128
-                      ? (i8 ? (many ? kv_read_kernel<128, true, kKvMany> : kv_read_kernel<128, true, 1>)
-                            : (many ? kv_read_kernel<128, false, kKvMany> : kv_read_kernel<128, false, 1>))
-                      : (i8 ? (many ? kv_read_kernel<64, true, kKvMany> : kv_read_kernel<64, true, 1>)
-                            : (many ? kv_read_kernel<64, false, kKvMany> : kv_read_kernel<64, false, 1>));
-    return launch(kernel, dim3(kv_grid(T, cache->kv_heads, cache->head_dim, many ? kKvMany : 1)), dim3(kKvThreads), 0,
+                      ? (i8 ? (many ? kv_read_kernel<128, true, kKvManyI8> : kv_read_kernel<128, true, 1>)
+                            : (many ? kv_read_kernel<128, false, kKvManyBf16> : kv_read_kernel<128, false, 1>))
+                      : (i8 ? (many ? kv_read_kernel<64, true, kKvManyI8> : kv_read_kernel<64, true, 1>)
+                            : (many ? kv_read_kernel<64, false, kKvManyBf16> : kv_read_kernel<64, false, 1>));
+    return launch(kernel, dim3(kv_grid(cache, T, !many ? 1 : i8 ? kKvManyI8 : kKvManyBf16)), dim3(kKvThreads), 0,
                   static_cast<cudaStream_t>(stream), c, b, k, k_stride, v, v_stride);
 }
 

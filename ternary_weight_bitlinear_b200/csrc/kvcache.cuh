@@ -15,10 +15,10 @@
 // step, so every reader of that row (and no other) gets NaN.
 //
 // Both kernels move each row once and are bound by HBM bytes (for a few rows
-// by latency).  A group of d/8 lanes takes one or four (row, head) pairs, 16 bytes a
-// lane; a warp looks up 32 sequences at once, a lane each, so a row costs two
+// by latency).  A group of d/8 lanes (int8: d/16) takes one or several (row, head) pairs, 16
+// bytes of the cache a lane; a warp looks up 32 sequences at once, a lane each, so a row costs two
 // rounds of dependent loads (its sequence, its page) before its own; the row's
-// maximum costs log2(d/8) shuffles.
+// maximum costs log2(d/16) shuffles.
 #pragma once
 
 #include <type_traits>
@@ -169,18 +169,23 @@ __device__ __forceinline__ uint2 kv_codes8(const uint4& x, float s) {
     return make_uint2(four(0), four(4));
 }
 
-// One row quantised by its group of LANES lanes.
+// One row quantised by its group of LANES lanes, 16 elements a lane.
 template <int LANES>
-__device__ __forceinline__ void kv_store_i8(const uint4& x, int8_t* dst, float* step, int part, bool live) {
-    uint32_t m = kv_absmax8(x);
+__device__ __forceinline__ void kv_store_i8(const uint4 (&x)[2], int8_t* dst, float* step, int part, bool live) {
+    uint32_t m = max(kv_absmax8(x[0]), kv_absmax8(x[1]));
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (!live) return;
     const bool finite = m < 0x7F80u;
     const float s = __fdiv_rn(127.0f, fmaxf(bf16_bits_to_float(m), kScaleFloor));
-    *reinterpret_cast<uint2*>(dst + part * 8) = finite ? kv_codes8(x, s) : make_uint2(0, 0);
+    const uint2 lo = kv_codes8(x[0], s), hi = kv_codes8(x[1], s);
+    *reinterpret_cast<uint4*>(dst + part * 16) = finite ? make_uint4(lo.x, lo.y, hi.x, hi.y) : make_uint4(0, 0, 0, 0);
     if (part == 0) *step = finite ? __frcp_rn(s) : __int_as_float(0x7FC00000);
 }
+
+// 16-byte vectors of bf16 a lane: one, or the two whose codes fill one.
+template <bool I8>
+constexpr int kKvVecs = I8 ? 2 : 1;
 
 // R rows a group, GROUPS apart, so neighbouring groups have neighbouring heads
 // and tokens.
@@ -188,7 +193,7 @@ template <int D, bool I8, int R>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCacheArgs c, const KvBatchArgs a,
                                                               const uint16_t* __restrict__ k, int64_t k_stride,
                                                               const uint16_t* __restrict__ v, int64_t v_stride) {
-    constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
+    constexpr int V = kKvVecs<I8>, LANES = D / (8 * V), GROUPS = kKvThreads / LANES;
     const int lane = threadIdx.x & 31, part = threadIdx.x % LANES;
     const int pairs = a.T * c.kv_heads;  // (row, head) pairs
     const int block0 = blockIdx.x * (GROUPS * R);
@@ -196,15 +201,18 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCacheArgs 
     pdl_wait();
     pdl_launch_dependents();
     if (warp0 >= pairs) return;  // warp-uniform
-    uint4 kx[R], vx[R];
+    uint4 kx[R][V], vx[R][V];
     int t[R], head[R];
 #pragma unroll
     for (int u = 0; u < R; ++u) {
         const int pair = min(first + u * GROUPS, pairs - 1);
         t[u] = c.by_heads.div(pair);
         head[u] = pair - t[u] * c.kv_heads;
-        kx[u] = __ldcg(reinterpret_cast<const uint4*>(k + t[u] * k_stride + head[u] * D) + part);
-        vx[u] = __ldcg(reinterpret_cast<const uint4*>(v + t[u] * v_stride + head[u] * D) + part);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            kx[u][e] = __ldcg(reinterpret_cast<const uint4*>(k + t[u] * k_stride + head[u] * D) + part * V + e);
+            vx[u][e] = __ldcg(reinterpret_cast<const uint4*>(v + t[u] * v_stride + head[u] * D) + part * V + e);
+        }
     }
     const KvWindow window(a, c.by_heads.div(warp0), lane);
 #pragma unroll
@@ -215,8 +223,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCacheArgs 
             kv_store_i8<LANES>(kx[u], static_cast<int8_t*>(c.k) + off, c.k_step + step_off, part, live);
             kv_store_i8<LANES>(vx[u], static_cast<int8_t*>(c.v) + off, c.v_step + step_off, part, live);
         } else if (live) {
-            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.k) + off) + part) = kx[u];
-            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.v) + off) + part) = vx[u];
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.k) + off) + part) = kx[u][0];
+            *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.v) + off) + part) = vx[u][0];
         }
     }
 }
@@ -240,8 +248,7 @@ template <int D, bool I8, int R>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCacheArgs c, const KvBatchArgs a,
                                                              uint16_t* __restrict__ k, int64_t k_stride,
                                                              uint16_t* __restrict__ v, int64_t v_stride) {
-    constexpr int LANES = D / 8, GROUPS = kKvThreads / LANES;
-    using Vec = typename std::conditional<I8, uint2, uint4>::type;  // eight elements as they are held
+    constexpr int V = kKvVecs<I8>, LANES = D / (8 * V), GROUPS = kKvThreads / LANES;
     using Held = typename std::conditional<I8, int8_t, uint16_t>::type;
     const int lane = threadIdx.x & 31, part = threadIdx.x % LANES;
     const int pairs = a.T * c.kv_heads;
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCacheArgs c
     pdl_launch_dependents();
     if (warp0 >= pairs) return;
     const KvWindow window(a, c.by_heads.div(warp0), lane);
-    Vec kx[R], vx[R];
+    uint4 kx[R], vx[R];  // as they are held
     float ks[R], vs[R];
     int64_t to_k[R], to_v[R];
     bool live[R];
@@ -261,8 +268,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCacheArgs c
         int64_t off, step_off;
         live[u] = window.place(c, a, t, head, &off, &step_off) && first + u * GROUPS < pairs;
         if (live[u]) {
-            kx[u] = __ldcg(reinterpret_cast<const Vec*>(static_cast<const Held*>(c.k) + off) + part);
-            vx[u] = __ldcg(reinterpret_cast<const Vec*>(static_cast<const Held*>(c.v) + off) + part);
+            kx[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const Held*>(c.k) + off) + part);
+            vx[u] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const Held*>(c.v) + off) + part);
             if constexpr (I8) {
                 ks[u] = __ldcg(c.k_step + step_off);
                 vs[u] = __ldcg(c.v_step + step_off);
@@ -274,16 +281,17 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCacheArgs c
 #pragma unroll
     for (int u = 0; u < R; ++u) {
         if (!live[u]) continue;
-        uint4 x, y;
+        uint4* const ko = reinterpret_cast<uint4*>(k + to_k[u]) + part * V;
+        uint4* const vo = reinterpret_cast<uint4*>(v + to_v[u]) + part * V;
         if constexpr (I8) {
-            x = kv_values8(kx[u], ks[u]);
-            y = kv_values8(vx[u], vs[u]);
+            ko[0] = kv_values8(make_uint2(kx[u].x, kx[u].y), ks[u]);
+            ko[1] = kv_values8(make_uint2(kx[u].z, kx[u].w), ks[u]);
+            vo[0] = kv_values8(make_uint2(vx[u].x, vx[u].y), vs[u]);
+            vo[1] = kv_values8(make_uint2(vx[u].z, vx[u].w), vs[u]);
         } else {
-            x = kx[u];
-            y = vx[u];
+            ko[0] = kx[u];
+            vo[0] = vx[u];
         }
-        *(reinterpret_cast<uint4*>(k + to_k[u]) + part) = x;
-        *(reinterpret_cast<uint4*>(v + to_v[u]) + part) = y;
     }
 }
 

@@ -493,38 +493,54 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
         : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
 }
 
-// ---- one row by a warp, position by position --------------------------------
+// ---- one row by a warp ---------------------------------------------------------
 // The (max, sum, vector) of one row over positions [j0, j1) straight from the
 // cache, D/32 dimensions a lane, bf16 pages: only the positions that the row
-// sees take part, whatever the others hold.
+// sees take part, whatever the others hold.  32 positions at a time: a lane
+// scores one, then the warp adds the values position by position.  (Seldom
+// needed; but a cache full of NaN sends every row here.)
 template <int D>
 __device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const uint16_t* qrow, int j0, int j1,
                                     float (&o)[D / 32], float* m_out, float* l_out) {
     constexpr int DL = D / 32;
     const int lane = threadIdx.x & 31;
-    float q[DL], m = -INFINITY, l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
 #pragma unroll
-    for (int e = 0; e < DL; ++e) {
-        q[e] = bf16_bits_to_float(__ldcg(qrow + lane * DL + e)) * a.qscale;
-        o[e] = 0.0f;
-    }
-    for (int j = j0; j < j1; ++j) {
-        const int page = kv_page(a.c, a.b, b, j), slot = a.c.by_page.mod(j);
-        if (page < 0) continue;
-        const int64_t off = page * a.c.sp + slot * a.c.ss + g * a.c.sh + lane * DL;
-        float x = 0.0f, v[DL];
+    for (int e = 0; e < DL; ++e) o[e] = 0.0f;
+    for (int j = j0; j < j1; j += 32) {
+        const int p = j + lane;
+        const int page = p < j1 ? kv_page(a.c, a.b, b, p) : -1;
+        const int64_t off = max(page, 0) * a.c.sp + a.c.by_page.mod(p) * a.c.ss + g * a.c.sh;
+        float x = 0.0f;
+        for (int e = 0; e < D; e += 8) {
+            const uint4 q8 = __ldcg(reinterpret_cast<const uint4*>(qrow + e));
+            const uint4 k8 = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.k) + off + e))
+                                       : make_uint4(0, 0, 0, 0);
+            const uint32_t qw[4] = {q8.x, q8.y, q8.z, q8.w}, kw[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
-        for (int e = 0; e < DL; ++e) {
-            x = fmaf(q[e], bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.k) + off + e)), x);
-            v[e] = bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.v) + off + e));
+            for (int y = 0; y < 4; ++y) {
+                x = fmaf(__uint_as_float(qw[y] << 16), __uint_as_float(kw[y] << 16), x);
+                x = fmaf(__uint_as_float(qw[y] & 0xFFFF0000u), __uint_as_float(kw[y] & 0xFFFF0000u), x);
+            }
         }
-        x = warp_sum_f(x);
-        const float mn = fmaxf(m, x);
-        const float alpha = m == mn ? 1.0f : exp2f(m - mn), p = mn == -INFINITY && x == x ? 0.0f : exp2f(x - mn);
-        l = fmaf(l, alpha, p);
-#pragma unroll
-        for (int e = 0; e < DL; ++e) o[e] = fmaf(p, v[e], o[e] * alpha);
+        x = page >= 0 ? x * a.qscale : -INFINITY;
+        const float mn = fmaxf(m, warp_max_f(x));
+        const float alpha = m == mn ? 1.0f : exp2f(m - mn);
+        const float w = page < 0 || (mn == -INFINITY && x == x) ? 0.0f : exp2f(x - mn);
+        l = fmaf(l, alpha, warp_sum_f(w));
         m = mn;
+#pragma unroll
+        for (int e = 0; e < DL; ++e) o[e] *= alpha;
+        const uint32_t some = __ballot_sync(0xffffffffu, page >= 0);
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const int64_t at = __shfl_sync(0xffffffffu, off, i);
+            if (!((some >> i) & 1u)) continue;
+#pragma unroll
+            for (int e = 0; e < DL; ++e)
+                o[e] = fmaf(wi, bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.v) + at + lane * DL + e)), o[e]);
+        }
     }
     *m_out = m;
     *l_out = l;

@@ -490,8 +490,8 @@ typedef struct {
  * included: row i of its n rows stands at position kv_len[b] - n + i, and
  * position p lies in page pages[b * max_pages + p / page_size], slot
  * p % page_size.  Sequences may have no rows or no positions.  Rows behind
- * cu_q[batch] (a padded batch) belong to no sequence: nothing of them is read
- * or written.  Entries of the table past a sequence's positions are not used.
+ * cu_q[batch] (a padded batch) belong to no sequence: they take no part, and
+ * their results are left as they were.  Entries of the table past a sequence's positions are not used.
  * Whatever the arrays hold, no access leaves the buffers: starts are cut to
  * the row buffers, lengths to max_pages * page_size, and a needed entry that
  * is no page of the cache records BL_ERR_PAGE in the device status (the
@@ -516,7 +516,7 @@ typedef struct {
  *   k, v       device bf16 [T, kv_heads, head_dim]; rows k_stride / v_stride
  *              elements apart (slices of a fused projection), heads contiguous;
  *              16-byte aligned, strides multiples of 8.
- * T >= 0 rows; no workspace. */
+ * T >= 0 rows, T * kv_heads < INT32_MAX - 1024; no workspace. */
 bl_status bitlinear_kv_write(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* k,
                              int64_t k_stride, const uint16_t* v, int64_t v_stride, int64_t T,
                              void* stream);
@@ -548,11 +548,15 @@ bl_status bitlinear_attn_paged_workspace_size(int64_t T, int64_t q_heads, int64_
  *   q, out     device bf16 [T, q_heads, head_dim]; rows q_stride / out_stride
  *              elements apart, heads contiguous; 16-byte aligned, strides
  *              multiples of 8.  Rows of no sequence are left as they were.
- *   scale      score multiplier, positive and finite (1/sqrt(head_dim) in the model).
+ *              out must not overlap q (BL_ERR_SHAPE); both may be slices of the
+ *              rows of one tensor.
+ *   scale      score multiplier, positive, scale * log2(e) finite (1/sqrt(head_dim)
+ *              in the model).
  *   workspace  device, 16-byte aligned, at least
  *              bitlinear_attn_paged_workspace_size bytes.  A workspace serves
  *              one call at a time; its contents need no initialisation and
- *              nothing in it is kept for the next call.
+ *              nothing in it is kept for the next call (but after
+ *              BL_ERR_TIMEOUT clear it before a captured call replays).
  * q_heads / kv_heads in 1 .. 128, T * q_heads <= INT32_MAX. */
 bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batch, const uint16_t* q,
                                int64_t q_stride, int64_t T, int64_t q_heads, float scale, int causal,

@@ -100,8 +100,9 @@ struct PagedAttnArgs {
 
 // ---- items ------------------------------------------------------------------
 // An item and this CTA's part of it, as the scheduler warp leaves it in shared
-// memory for the other roles.
-struct PaItem {
+// memory for the other roles.  (64 bytes in aligned words: as 14 loose words the
+// items cost chunks over an int8 cache 4%, 270 -> 282 us.)
+struct alignas(16) PaItem {
     int b, g;        // sequence, key/value head; b < 0: no more items
     int row;         // first token's row in the batch
     int tokens;      // tokens of the item
@@ -114,7 +115,6 @@ struct PaItem {
     int len;         // positions of the sequence
     int slot;        // running number of its first Q tile; a pair whose first sub-tile has no tile here loads the
     int nq;          // second only (nq of them, 0 without tiles)
-    int pad[2];
 };
 constexpr int kPaItems = 4;      // ring of items
 
@@ -185,15 +185,15 @@ struct PaWalk {
             slot += it.nq;
             const bool mine = lo < hi || (nt == 0 && from <= 0);
             at += c;
-            if (++i == items) {
+            // (the next item is looked up when there is one in the share: a padded batch may end in many empty sequences)
+            if (at < u1 && ++i == items) {
                 i = 0;
                 if (++g == a.c.kv_heads) {
                     g = 0;
-                    while (++b < a.b.batch) {
-                        load();
-                        if (s.n > 0) break;
-                    }
-                    if (b >= a.b.batch) at = u1;  // past the last item
+                    ++b;  // (a share that goes on has a sequence with rows left)
+                    if (b < a.b.batch) load();
+                    if (b < a.b.batch && s.n <= 0 && (b = kv_next(a.b, b)) < a.b.batch) load();
+                    if (b >= a.b.batch) at = u1;
                 }
             }
             if (mine) return true;
@@ -498,7 +498,8 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
 // cache, D/32 dimensions a lane, bf16 pages: only the positions that the row
 // sees take part, whatever the others hold.  32 positions at a time: a lane
 // scores one, then the warp adds the values position by position.  (Seldom
-// needed; but a cache full of NaN sends every row here.)
+// needed: 9 us for each 32 positions
+// of a row where every warp of the GPU is at it.)
 template <int D>
 __device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const uint16_t* qrow, int j0, int j1,
                                     float (&o)[D / 32], float* m_out, float* l_out) {
@@ -511,12 +512,12 @@ __device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const 
         const int p = j + lane;
         const int page = p < j1 ? kv_page(a.c, a.b, b, p) : -1;
         const int64_t off = max(page, 0) * a.c.sp + a.c.by_page.mod(p) * a.c.ss + g * a.c.sh;
+        const uint4* k8 = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.k) + off);
         float x = 0.0f;
-        for (int e = 0; e < D; e += 8) {
-            const uint4 q8 = __ldcg(reinterpret_cast<const uint4*>(qrow + e));
-            const uint4 k8 = page >= 0 ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.k) + off + e))
-                                       : make_uint4(0, 0, 0, 0);
-            const uint32_t qw[4] = {q8.x, q8.y, q8.z, q8.w}, kw[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+        for (int e = 0; e < D / 8; ++e) {
+            const uint4 qv = __ldg(reinterpret_cast<const uint4*>(qrow) + e), kv = __ldcg(k8 + e);
+            const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, kw[4] = {kv.x, kv.y, kv.z, kv.w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 x = fmaf(__uint_as_float(qw[y] << 16), __uint_as_float(kw[y] << 16), x);
@@ -532,18 +533,54 @@ __device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const 
 #pragma unroll
         for (int e = 0; e < DL; ++e) o[e] *= alpha;
         const uint32_t some = __ballot_sync(0xffffffffu, page >= 0);
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < 32; ++i) {
+            // (a lane without a page stands at page 0, which every cache has)
+            const uint16_t* v = static_cast<const uint16_t*>(a.c.v) + __shfl_sync(0xffffffffu, off, i) + lane * DL;
             const float wi = __shfl_sync(0xffffffffu, w, i);
-            const int64_t at = __shfl_sync(0xffffffffu, off, i);
+            uint32_t vw[DL / 2];
+            if constexpr (DL == 4) {
+                const uint2 y = __ldcg(reinterpret_cast<const uint2*>(v));
+                vw[0] = y.x;
+                vw[1] = y.y;
+            } else {
+                vw[0] = __ldcg(reinterpret_cast<const uint32_t*>(v));
+            }
             if (!((some >> i) & 1u)) continue;
 #pragma unroll
             for (int e = 0; e < DL; ++e)
-                o[e] = fmaf(wi, bf16_bits_to_float(__ldcg(static_cast<const uint16_t*>(a.c.v) + at + lane * DL + e)), o[e]);
+                o[e] = fmaf(wi, __uint_as_float((e & 1) ? vw[e / 2] & 0xFFFF0000u : vw[e / 2] << 16), o[e]);
         }
+        bool done = true;  // a NaN stays one: nothing changes any more
+#pragma unroll
+        for (int e = 0; e < DL; ++e) done = done && o[e] != o[e];
+        if (__all_sync(0xffffffffu, done)) break;
     }
     *m_out = m;
     *l_out = l;
+}
+
+// The last position of [j0, j1) whose value row (bf16 pages) holds an infinity
+// or NaN, for a whole warp; -1 when none does.
+template <int D>
+__device__ __noinline__ int pa_last_non_finite(const PagedAttnArgs& a, int b, int g, int j0, int j1) {
+    constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a row, rows at once
+    const int lane = threadIdx.x & 31;
+    for (int j = j1; j > j0; j -= 4 * PER) {
+        int last = -1;
+#pragma unroll
+        for (int u = 3; u >= 0; --u) {
+            const int p = j - 1 - u * PER - lane / LANES;
+            const int page = p >= j0 ? kv_page(a.c, a.b, b, p) : -1;
+            if (page < 0) continue;
+            const int64_t off = page * a.c.sp + a.c.by_page.mod(p) * a.c.ss + g * a.c.sh;
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.v) + off) + lane % LANES);
+            if (kv_absmax8(v) >= 0x7F80u) last = p;
+        }
+        last = __reduce_max_sync(0xffffffffu, last);
+        if (last >= 0) return last;
+    }
+    return -1;
 }
 
 // ---- the kernel -----------------------------------------------------------------
@@ -904,7 +941,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         setmaxnreg_inc<C::kRegsSoft>();
         const int w = (warp - 4) >> 2, quad = warp & 3;
         const int row = quad * 32 + lane;
-        const int tok = a.by_group.div(row), hh = a.by_group.mod(row);
+        const int tok = a.by_group.div(row);
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const uint32_t ts = tmem + lanes + 128u * w, to_o = tmem + lanes + 256u + 128u * w;
         float2* ml = reinterpret_cast<float2*>(sm + C::kOffMl);
@@ -1153,6 +1190,13 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     // an infinity or NaN came out.  Where it stands in a position that the row does not see (its
                     // probability there is zero, the product is not), the row is computed from what it sees alone
                     uint32_t bad = __ballot_sync(0xffffffffu, live && !(poison == 0.0f));
+                    if (bad) {
+                        const int own = pair && w == 0 ? item->end0 : end;  // the product's last 16 may go beyond
+                        const int last = pa_last_non_finite<D>(
+                            a, item->b, item->g, max(__reduce_min_sync(0xffffffffu, vend), t0 * kPaTile),
+                            min(min(end, own + 15), t1 * kPaTile));
+                        bad &= __ballot_sync(0xffffffffu, vend <= last);
+                    }
                     __syncwarp();
                     while (bad) {
                         const int src = __ffs(bad) - 1;

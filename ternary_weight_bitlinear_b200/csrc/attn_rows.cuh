@@ -15,10 +15,10 @@
 //    tcgen05 tile has 64 rows at least and would also pass scores and
 //    probabilities through tensor memory), keeps the running maximum, sum and
 //    output of its positions, and feeds the probabilities of one product to the
-//    next without leaving registers.  int8 codes become bf16 (exactly) in registers, in the order
-//    in which shared memory gives them up in whole 16-byte words: the
-//    positions and dimensions of a product may stand in any order as long as
-//    both operands agree.
+//    next without leaving registers.  int8 codes become bf16 (exactly) in
+//    registers, in the order in which shared memory gives them up in whole
+//    16-byte words: the positions and dimensions of a product may stand in any
+//    order as long as both operands agree.
 //  * Items ((sequence, head, 16 rows) times their chunks) are shared out
 //    evenly over the CTAs as in attn_paged.cuh.  The warps of a CTA merge
 //    through shared memory; of the CTAs that hold parts of one item the last
@@ -154,14 +154,14 @@ struct RwWalk {
                 it.unit_lo = (int)(first & 0xFFFFFFFF);
             }
             at += c;
-            if (++i == items) {
+            // (the next item is looked up when there is one in the share: a padded batch may end in many empty sequences)
+            if (at < u1 && ++i == items) {
                 i = 0;
                 if (++g == a.c.kv_heads) {
                     g = 0;
-                    while (++b < a.b.batch) {
-                        load();
-                        if (s.n > 0) break;
-                    }
+                    ++b;  // (a share that goes on has a sequence with rows left)
+                    if (b < a.b.batch) load();
+                    if (b < a.b.batch && s.n <= 0 && (b = kv_next(a.b, b)) < a.b.batch) load();
                     if (b >= a.b.batch) at = u1;
                 }
             }
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
     pdl_launch_dependents();
     // this CTA's counters (an item that begins here and goes on in others; a group that its parts are first of): this
     // launch's, and nothing counted yet
-    if (threadIdx.x < 3) st_counter(threadIdx.x == 0 ? counters + blockIdx.x : counters + gridDim.x + 2 * blockIdx.x + threadIdx.x - 1, epoch << 32);
+    if (threadIdx.x < 3) st_counter(threadIdx.x == 0 ? counters + blockIdx.x : counters + gridDim.x + 2 * blockIdx.x + threadIdx.x - 1, epoch);
     pa_plan<RwCut<NR>>(a, plan, seq, warp_sums);
 
     bool ok = true;
@@ -691,10 +691,12 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                 ok = __all_sync(0xffffffffu, mbar_wait(got_bar, merges & 1u));
                 if (!ok) break;
                 const unsigned bad = *reinterpret_cast<volatile unsigned*>(bad_rows);
+                const int last = bad ? pa_last_non_finite<D>(a, item->b, item->g, max(vmin, t0 * kRwChunk), min(end, t1 * kRwChunk)) : -1;
                 for (int r = w; bad && r < rows; r += W) {
                     if (!((bad >> r) & 1)) continue;
                     const int row = item->row0 + r, tok = a.by_group.div(row);
                     const int ve = a.causal ? min(max(item->vbase + tok + 1, 0), item->len) : item->len;
+                    if (last < ve) continue;
                     const int64_t at = item->q0 + tok, head = head0 + a.by_group.mod(row);
                     float x[D / 32], m2, l2;
                     pa_row<D>(a, item->b, item->g, a.q + at * a.q_stride + head * D, t0 * kRwChunk,
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                     ++sent;
                     if (!ok) return false;
                     if (ct == 0) {
-                        const unsigned long long tag = epoch & 0xFFFFFFFFull;
+                        const unsigned long long tag = epoch >> 32;
                         unsigned long long old = arrive_counter(ctr);
                         for (int tries = 0; old >> 32 != tag && tries < 64; ++tries) {
                             for (int spin = 0; spin < (1 << 16) && ld_acquire(ctr) >> 32 != tag; ++spin) {}

@@ -807,7 +807,7 @@ bl_status kv_check(const bl_kv_cache* c, const bl_kv_batch* b, int64_t T, KvCach
     if (b->batch < 0 || b->batch >= INT32_MAX || b->max_pages < 0 ||
         b->max_pages > kKvMaxPositions / c->page_size)
         return BL_ERR_SHAPE;
-    if (T < 0 || T > INT32_MAX / c->kv_heads) return BL_ERR_SHAPE;
+    if (T < 0 || T > kKvMaxPairs / c->kv_heads) return BL_ERR_SHAPE;
     const int64_t unit = i8 ? 16 : 8, most = ((int64_t)1 << 40) / (i8 ? 1 : 2);
     for (const int64_t s : {c->stride_page, c->stride_slot, c->stride_head}) {
         if (s <= 0 || s >= most) return BL_ERR_SHAPE;
@@ -844,6 +844,17 @@ bl_status kv_rows_check(const void* p, int64_t stride, int64_t width) {
     if (stride < width || stride > INT64_MAX / INT32_MAX) return BL_ERR_SHAPE;
     if (!p) return BL_ERR_NULL;
     return aligned16(p) && stride % 8 == 0 ? BL_OK : BL_ERR_ALIGN;
+}
+
+// Whether two row buffers [T, width] share elements (equal strides: buffers that
+// take turns within the rows of one tensor do not).
+bool rows_overlap(const uint16_t* p, int64_t p_stride, const uint16_t* q, int64_t q_stride, int64_t T, int64_t width) {
+    const bool p_first = reinterpret_cast<uintptr_t>(p) <= reinterpret_cast<uintptr_t>(q);
+    const int64_t gap = (int64_t)((p_first ? reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)
+                                           : reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) / 2);
+    if (gap - width >= (T - 1) * (p_first ? p_stride : q_stride)) return false;  // one ends before the other begins
+    if (p_stride != q_stride || T == 1) return true;
+    return gap % p_stride < width || gap % p_stride > p_stride - width;
 }
 
 // Rows a group of lanes takes in turn: several keep enough loads in flight where
@@ -932,7 +943,7 @@ bl_status attn_rows_launch(PagedAttnArgs& a, int dev, const DeviceInfo& info, un
         return BL_ERR_CUDA;
     a.part_rows = kRwRows;
     return launch(attn_rows_kernel<D, I8, NR>, dim3((unsigned)info.sms), dim3(C::kThreads), (size_t)C::kSmem, stream, map_k,
-                  map_v, (const PagedAttnArgs&)a, counters, next_epoch());
+                  map_v, (const PagedAttnArgs&)a, counters, ((next_epoch() & 0xFFFFFFFFull) | 0x80000000ull) << 32);
 }
 
 template <int D, bool I8>
@@ -1480,11 +1491,12 @@ bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batc
     bl_status st;
     if ((st = kv_check(cache, batch, T, &a.c, &a.b)) != BL_OK) return st;
     if ((st = attn_paged_check(T, q_heads, cache->kv_heads, cache->head_dim)) != BL_OK) return st;
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return BL_ERR_SHAPE;
+    if (!(scale > 0.0f) || !std::isfinite(scale * kLog2e)) return BL_ERR_SHAPE;
     if (T == 0 || batch->batch == 0) return BL_OK;
     const int64_t width = q_heads * cache->head_dim;
     if ((st = kv_rows_check(q, q_stride, width)) != BL_OK || (st = kv_rows_check(out, out_stride, width)) != BL_OK)
         return st;
+    if (rows_overlap(q, q_stride, out, out_stride, T, width)) return BL_ERR_SHAPE;
     int dev;
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != BL_OK) return st;

@@ -29,6 +29,7 @@ namespace bl {
 
 constexpr int kKvThreads = 128;
 constexpr int64_t kKvMaxPositions = 1 << 30;  // of a page table's row: position arithmetic stays in 32 bits
+constexpr int64_t kKvMaxPairs = INT32_MAX - 1024;  // (row, key/value head) pairs: a grid's last block stays in 32 bits too
 
 // Division of x < 2^31 by a divisor known on the host: with s = ceil(log2 d)
 // and m = ceil(2^(31 + s) / d), m d exceeds 2^(31 + s) by less than d <= 2^s,
@@ -82,16 +83,32 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatchArgs& a, int b) {
 
 // The sequence of row t, searched by a whole warp: the number of starts
 // cu_q[1..batch] at or below t (batch when no sequence has the row).  The
-// starts are in ascending order, so empty sequences are passed over.
+// starts are in ascending order, so empty sequences are passed over; each
+// round's 32 probes leave a 32nd of them.
 __device__ __forceinline__ int kv_seq_of_row(const KvBatchArgs& a, int t, int lane) {
-    int count = 0;
-    for (int i = 0; i < a.batch; i += 32) {
-        const bool below = i + lane < a.batch && __ldcg(a.cu_q + 1 + i + lane) <= t;
-        const uint32_t m = __ballot_sync(0xffffffffu, below);
-        count += __popc(m);
-        if (m != 0xffffffffu) break;
+    uint32_t lo = 0, n = (uint32_t)a.batch;  // the answer lies in [lo, lo + n]
+    while (n > 0) {
+        const uint32_t step = (n + 31) / 32, at = (lane + 1) * step - 1;
+        const bool below = at < n && __ldcg(a.cu_q + 1 + lo + at) <= t;
+        const uint32_t c = __popc(__ballot_sync(0xffffffffu, below)) * step;
+        lo += c;
+        n = min(step - 1, n - c);
     }
-    return count;
+    return (int)lo;
+}
+
+// The first sequence after b that has rows (batch: none).  Eight at a time: a
+// step's batch may be padded with many that have none.
+__device__ __forceinline__ int kv_next(const KvBatchArgs& a, int b) {
+    for (++b; b < a.batch; b += 8) {
+        int cu[9];
+#pragma unroll
+        for (int i = 0; i < 9; ++i) cu[i] = min(max(__ldcg(a.cu_q + min(b + i, a.batch)), 0), a.T);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (cu[i + 1] > cu[i]) return b + i;
+    }
+    return a.batch;
 }
 
 // Page of position p of sequence b, or -1 (recorded in the status word) when
@@ -127,7 +144,7 @@ struct KvWindow {
         KvSeq q = {__shfl_sync(0xffffffffu, s.q0, i), __shfl_sync(0xffffffffu, s.n, i), __shfl_sync(0xffffffffu, s.len, i)};
         int b = base + i;
         if (past) {
-            while (b < a.batch && __ldcg(a.cu_q + b + 1) <= t) ++b;
+            while (b < a.batch && __ldcg(a.cu_q + b + 1) <= t) b = kv_next(a, b);
             if (b < a.batch) q = kv_seq(a, b);
         }
         const int pos = q.len - q.n + (t - q.q0);

@@ -117,7 +117,7 @@ def attention_error_bound(want, absv, mag, seen, d):
     return 2.0 ** -8 * np.abs(want) + rel[..., None] * absv + 2.0 ** -126
 
 
-def run_attention(p, H, causal, seed, q_std=1.0, scale=None, graph=False):
+def run_attention(p, H, causal, seed, q_std=1.0, scale=None):
     """bitlinear_attn_paged on the batch `p` against the oracle."""
     d = p.d
     scale = float(np.float32(d ** -0.5 if scale is None else scale))
@@ -143,3 +143,14 @@ def run_attention(p, H, causal, seed, q_std=1.0, scale=None, graph=False):
         *w, err[w], bound[w], got[w], want[w])
     assert (got[:used][seen[:used] == 0] == 0).all(), "a row that sees nothing must be zeros"
     return got, od
+
+
+def padded_batch(count, most_new, most_len, seed):
+    """New rows and positions of `count` sequences, most of them without rows: here and there, a run of them longer
+    than anything looks at at once, and the batch's end."""
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(1, most_len + 1, count)
+    new = np.minimum(rng.integers(0, most_new + 1, count), lens)
+    new[count // 4:count // 4 + 300] = 0
+    new[-(count // 5):] = 0
+    return [int(x) for x in new], [int(x) for x in lens]

@@ -6,7 +6,7 @@ import torch
 
 import ternary_weight_bitlinear_b200 as B
 from gpu_util import bf16_dev, bf16_host, f32_of_bf16
-from kv_util import Paged, attention_error_bound, bf16_values, bits, run_attention
+from kv_util import Paged, attention_error_bound, bf16_values, bits, padded_batch, run_attention
 from ternary_weight_bitlinear_b200 import workloads as WL
 
 pytestmark = pytest.mark.gpu
@@ -88,6 +88,25 @@ def test_many_decode_rows_and_one_chunk(H, Hkv, d, fmt, guard):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("H,Hkv,d", [(4, 4, 64), (40, 2, 64), (100, 1, 128)])
+def test_many_sequences(H, Hkv, d, fmt, guard):
+    """More sequences than a CTA has threads, runs of empty ones among them and behind them: few rows a sequence and
+    many (of the heads)."""
+    new, lens = padded_batch(1100, 1, 70, seed=H)
+    p = Paged(guard, new, lens, 16, Hkv, d, fmt, seed=H + 9, pad=3)
+    run_attention(p, H, True, seed=H + 10)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n,group,L", [(1, 4, 2051), (1, 12, 2051), (2, 4, 4500), (1, 4, 7001), (1, 16, 30000),
+                                       (8, 4, 2051), (8, 4, 20001), (70, 4, 20001)])
+def test_one_sequence_over_many_parts(n, group, L, fmt, guard):
+    """One key/value head: the positions of a single item are shared out over most of the GPU, or all of it."""
+    p = Paged(guard, [n], [L], 64, 1, 128 if n > 1 or group == 4 else 64, fmt, seed=L + n)
+    run_attention(p, group, True, seed=L + group)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
 def test_peaked_scores(fmt, guard):
     # large queries: the softmax is close to one-hot and the running maximum moves
     p = Paged(guard, [1, 64], [700, 300], 16, 5, 128, fmt, seed=77)
@@ -142,6 +161,43 @@ def test_non_finite_rows_reach_only_rows_that_see_them(what, fmt, guard):
     ok = np.isfinite(want)
     bound = attention_error_bound(np.where(ok, want, 0), np.where(ok, absv, 0), np.where(np.isfinite(mag), mag, 0), seen, d)
     assert (np.abs(a - np.where(ok, want, 0))[ok] <= bound[ok]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n,L", [(4, 4), (4, 40), (4, 5000), (64, 64), (64, 3000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_among_the_new_rows(n, L, d, fmt, guard):
+    """The last new row is NaN in keys and values: the others, which do not see it, are as without it, whichever
+    kernel computes them and however the positions are shared out."""
+    p = Paged(guard, [n], [L], 16, 1, d, fmt, seed=L + d)
+    at = p.pages[0][(L - 1) // 16], (L - 1) % 16
+    if fmt == "int8":
+        p.ks[at] = p.vs[at] = np.nan
+    else:
+        p.kc[at] = p.vc[at] = np.nan
+    p.upload()
+    q = bf16_values(np.random.default_rng(n), (n, 4, d))
+    scale = np.float32(d ** -0.5)
+    got = f32_of_bf16(bf16_host(B.bitlinear_attn_paged(bf16_dev(bits(q)), p.cache, p.batch, float(scale))))
+    assert np.isnan(got[-1]).all()
+    import oracle.kvcache as OK
+    k, v = (x[:-1] for x in p.sequence(0))
+    want, absv, mag, seen = OK.attention(q[:-1], [k], [v], np.array([0, n - 1]), [L - 1], scale, True,
+                                         np.zeros_like(q[:-1]))
+    assert (np.abs(got[:-1] - want) <= attention_error_bound(want, absv, mag, seen, d)).all()
+
+
+def test_rows_that_overlap_are_refused(guard):
+    p = Paged(guard, [3], [20], 16, 1, 64, "bf16", seed=85)
+    w = torch.zeros((4, 8, 64), dtype=torch.bfloat16, device="cuda")
+    for q, out in ((w[:3, :4], w[:3, :4]), (w[:3, :4], w[:3, 3:7]), (w[:3, 4:], w[1:, 3:7]), (w[1:, :4], w[:3, 1:5])):
+        with pytest.raises(B.BitLinearError):
+            B.bitlinear_attn_paged(q, p.cache, p.batch, 0.125, out=out)
+    q = torch.randn((3, 4, 64), device="cuda").to(torch.bfloat16)
+    w[:3, :4] = q
+    B.bitlinear_attn_paged(w[:3, :4], p.cache, p.batch, 0.125, out=w[:3, 4:])
+    B.bitlinear_attn_paged(w[:3, :4], p.cache, p.batch, 0.125, out=w[1:, 4:])
+    assert torch.equal(w[1:, 4:], B.bitlinear_attn_paged(q, p.cache, p.batch, 0.125))
 
 
 def test_every_score_minus_infinity_is_nan(guard):

@@ -7,7 +7,7 @@ import torch
 import oracle.kvcache as OK
 import ternary_weight_bitlinear_b200 as B
 from gpu_util import bf16_dev, bf16_host, f32_of_bf16
-from kv_util import Paged, bf16_values, bits
+from kv_util import Paged, bf16_values, bits, padded_batch
 
 pytestmark = pytest.mark.gpu
 
@@ -83,6 +83,28 @@ def test_write_then_read(case, fmt, guard):
             x = OK.dequantise(pages[page_, slot], steps[0][page_, slot]) if p.i8 else pages[page_, slot]
             ref[r] = torch.from_numpy(x).to(torch.bfloat16).float().numpy()
         assert same(f32_of_bf16(bf16_host(got)), ref)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("heads,d", [(1, 64), (2, 128)])
+@pytest.mark.parametrize("count,most", [(33, 3), (1100, 2), (1025, 40)])
+def test_many_sequences(count, most, heads, d, fmt, guard):
+    """More sequences than are looked at at once, with runs of empty ones; the last has rows for several a group."""
+    new, lens = padded_batch(count, most, 50, seed=count + d)
+    p = Paged(guard, new, lens, 16, heads, d, fmt, seed=count, pad=9, poison=False)
+    k, v, kd, vd = rows_of(p, seed=count + 1)
+    B.bitlinear_kv_write(kd, vd, p.cache, p.batch)
+    want = expect_write(p, k, v)
+    for got, w, what in zip(p.device_pages(), want, ("k", "v", "k steps", "v steps")):
+        assert same(got, w), what
+    used = int(p.cu[-1])
+    ko, vo = B.bitlinear_kv_read(p.cache, p.batch, T=p.T)
+    at = np.array([(page, slot) for _, _, _, page, slot in OK.places(p.cu, p.lens, p.pages, p.page)]).T
+    for got, x, steps in ((ko, want[0], want[2:3]), (vo, want[1], want[3:4])):
+        x = x[at[0], at[1]]
+        x = OK.dequantise(x, steps[0][at[0], at[1]]) if p.i8 else x
+        got = f32_of_bf16(bf16_host(got))
+        assert same(got[:used], torch.from_numpy(x).to(torch.bfloat16).float().numpy()) and not got[used:].any()
 
 
 def test_codes_are_the_activation_quantisers(guard):

@@ -59,7 +59,7 @@ def write(c, b, k=A, ks=640, v=A, vs=640, T=3, fn="bitlinear_kv_write"):
     return getattr(B.lib(), fn)(ctypes.byref(c), ctypes.byref(b), k, ks, v, vs, T, None)
 
 
-def attend(c, b, q=A, qs=2560, T=3, heads=20, scale=0.1, causal=1, out=A, os=2560, ws=A, wsb=1 << 40):
+def attend(c, b, q=A, qs=2560, T=3, heads=20, scale=0.1, causal=1, out=0x4000000, os=2560, ws=A, wsb=1 << 40):
     return B.lib().bitlinear_attn_paged(ctypes.byref(c), ctypes.byref(b), q, qs, T, heads, scale, causal, out, os, ws,
                                         wsb, None)
 
@@ -77,6 +77,7 @@ def test_rows_are_checked(fn):
     c, b = cache(), batch()
     assert write(c, b, T=-1, fn=fn) == SHAPE
     assert write(c, b, T=2 ** 31, fn=fn) == SHAPE
+    assert write(c, b, T=(2 ** 31 - 1024) // 5 + 1, fn=fn) == SHAPE  # more (row, head) pairs than 32 bits hold
     assert write(c, b, ks=632, fn=fn) == SHAPE          # rows that overlap
     assert write(c, b, vs=644, fn=fn) == ALIGN
     assert write(c, b, k=None, fn=fn) == NULL
@@ -94,12 +95,20 @@ def test_attention_is_checked():
     assert attend(c, b, heads=5 * 129, qs=5 * 129 * 128, os=5 * 129 * 128) == SHAPE
     assert attend(c, b, heads=0) == SHAPE
     assert attend(c, b, T=2 ** 27) == SHAPE              # T * heads past INT32_MAX
-    for scale in (0.0, -1.0, float("inf"), float("nan")):
+    for scale in (0.0, -1.0, float("inf"), float("nan"), 3e38):
         assert attend(c, b, scale=scale) == SHAPE
     assert attend(c, b, qs=2552) == SHAPE
     assert attend(c, b, os=2564) == ALIGN
     assert attend(c, b, q=None) == NULL
     assert attend(c, b, out=A + 2) == ALIGN
+    for out in (A, A + 2 * 2560 * 2, A - 2 * 2544):      # q's rows, one of them, the end of one
+        assert attend(c, b, out=out) == SHAPE
+    assert attend(c, b, qs=5120, os=5120, out=A + 2 * 2552) == SHAPE
+    assert attend(c, b, qs=2560, os=5120, out=A + 2 * 5120) == SHAPE
+    for out in (A + 3 * 2 * 2560, A - 3 * 2 * 2560):     # behind it, before it
+        assert attend(c, b, out=out, ws=None) in (WORKSPACE, DEVICE)
+    for out in (A + 2 * 2560, A - 2 * 2560, A + 2 * 7680):  # in turns within rows of 5120
+        assert attend(c, b, qs=5120, os=5120, out=out, ws=None) in (WORKSPACE, DEVICE)
     assert attend(c, b, T=0, q=None, out=None, ws=None, wsb=0) == 0
     n = ctypes.c_size_t()
     assert B.lib().bitlinear_attn_paged_workspace_size(3, 20, 5, 128, None) == NULL

@@ -882,14 +882,22 @@ bl_status attn_paged_check(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t
 }
 
 // 4-D tensor (innermost contiguous), elements of elem_bytes; strides in elements.
+// A load that misses L2 brings whole lines of up to `run` bytes: no more than
+// what lies together, since the bytes beside a row are another head's, for
+// another CTA at another time (int8 rows of 128 bytes, 64 sequences of 3900
+// positions: 256-byte lines read 465 MB and take 82 us,
+// 128-byte ones 326 MB and 71 us).
 bool make_map_4d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes, const void* ptr,
                  const int64_t (&dims)[4], const int64_t (&strides)[3], const int (&box)[4],
-                 CUtensorMapSwizzle swizzle) {
+                 CUtensorMapSwizzle swizzle, int64_t run) {
     EncodeTiledFn fn = encode_tiled();
     if (!fn) {
         snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled is unavailable");
         return false;
     }
+    const CUtensorMapL2promotion promotion = run >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                             : run >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                          : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
     cuuint64_t d[4], st[3];
     cuuint32_t bx[4], es[4] = {1, 1, 1, 1};
     for (int i = 0; i < 4; ++i) {
@@ -898,7 +906,7 @@ bool make_map_4d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes,
         if (i < 3) st[i] = (cuuint64_t)(strides[i] * elem_bytes);
     }
     const CUresult r = fn(map, type, 4, const_cast<void*>(ptr), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled failed (%d)", (int)r);
         return false;
@@ -924,6 +932,12 @@ PagedWs attn_paged_ws(int64_t T, int64_t group, int64_t head_dim, int sms) {
     return w;
 }
 
+// Bytes of a key/value head's rows that lie together: a row, or as many as there
+// are where the slots follow one another.
+int64_t kv_run(const KvCacheArgs& c, int64_t d, int64_t elem_bytes) {
+    return (c.ss == d ? c.page_size : 1) * d * elem_bytes;
+}
+
 // Few rows against each position (attn_rows.cuh): 16 a sequence and key/value
 // head on average.  (The lengths themselves are on the device: either kernel
 // is right for every batch.)
@@ -935,8 +949,9 @@ bl_status attn_rows_launch(PagedAttnArgs& a, int dev, const DeviceInfo& info, un
     const int kb[4] = {I8 ? D : 64, 1, std::min(a.box, kRwChunk), 1};
     const CUtensorMapDataType kt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     const CUtensorMapSwizzle sw = I8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw) ||
-        !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw))
+    const int64_t run = kv_run(a.c, D, I8 ? 1 : 2);
+    if (!make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw, run) ||
+        !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw, run))
         return BL_ERR_CUDA;
     using C = RwCfg<D, I8, NR>;
     if (prepare_kernel(reinterpret_cast<const void*>(attn_rows_kernel<D, I8, NR>), dev, info, C::kThreads, C::kSmem) < 0)
@@ -969,9 +984,10 @@ bl_status attn_paged_launch(PagedAttnArgs& a, void* workspace, int dev, const De
     const int kb[4] = {I8 ? D : 64, 1, a.box, 1};
     const CUtensorMapDataType kt = I8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     const CUtensorMapSwizzle sw = I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
-    if (!make_map_4d(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw) ||
-        !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw))
+    const int64_t run = kv_run(a.c, D, I8 ? 1 : 2);
+    if (!make_map_4d(&map_q, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, a.q, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B, (int64_t)a.group * D * 2) ||
+        !make_map_4d(&map_k, kt, I8 ? 1 : 2, a.c.k, kd, ks, kb, sw, run) ||
+        !make_map_4d(&map_v, kt, I8 ? 1 : 2, a.c.v, kd, ks, kb, sw, run))
         return BL_ERR_CUDA;
     using C = PaCfg<D, I8>;
     if (prepare_kernel(reinterpret_cast<const void*>(attn_paged_kernel<D, I8>), dev, info, C::kThreads, C::kSmem) < 0)

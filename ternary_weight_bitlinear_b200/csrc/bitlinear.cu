@@ -804,7 +804,7 @@ bl_status kv_check(const bl_kv_cache* c, const bl_kv_batch* b, int64_t T, KvCach
     if (c->num_pages <= 0 || c->num_pages > INT32_MAX || c->page_size <= 0 || c->page_size % 16 != 0 ||
         c->page_size > (1 << 20) || c->kv_heads <= 0 || c->kv_heads > 65535)
         return BL_ERR_SHAPE;
-    if (b->batch < 0 || b->batch >= INT32_MAX || b->max_pages < 0 ||
+    if (b->batch < 0 || b->batch > INT32_MAX - 1024 || b->max_pages < 0 ||
         b->max_pages > kKvMaxPositions / c->page_size)
         return BL_ERR_SHAPE;
     if (T < 0 || T > kKvMaxPairs / c->kv_heads) return BL_ERR_SHAPE;
@@ -884,9 +884,9 @@ bl_status attn_paged_check(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t
 // 4-D tensor (innermost contiguous), elements of elem_bytes; strides in elements.
 // A load that misses L2 brings whole lines of up to `run` bytes: no more than
 // what lies together, since the bytes beside a row are another head's, for
-// another CTA at another time (int8 rows of 128 bytes, 64 sequences of 3900
-// positions: 256-byte lines read 465 MB and take 82 us,
-// 128-byte ones 326 MB and 71 us).
+// another CTA at another time (int8 rows of 128 bytes, 64 sequences of 3800
+// positions: 256-byte lines read 465 MB and take 82 us, 128-byte ones 326 MB
+// and 71 us).
 bool make_map_4d(CUtensorMap* map, CUtensorMapDataType type, int64_t elem_bytes, const void* ptr,
                  const int64_t (&dims)[4], const int64_t (&strides)[3], const int (&box)[4],
                  CUtensorMapSwizzle swizzle, int64_t run) {
@@ -938,9 +938,14 @@ int64_t kv_run(const KvCacheArgs& c, int64_t d, int64_t elem_bytes) {
     return (c.ss == d ? c.page_size : 1) * d * elem_bytes;
 }
 
-// Few rows against each position (attn_rows.cuh): 16 a sequence and key/value
-// head on average.  (The lengths themselves are on the device: either kernel
-// is right for every batch.)
+// Few rows against each position (attn_rows.cuh): up to NR a sequence and
+// key/value head on average, 8 (a product's columns) or 16.  The lengths
+// themselves are on the device: either kernel is right for every batch.  With
+// more rows the tensor-memory kernel is mostly faster (20/5 heads of 128 over
+// 2000 positions, 16 rows an item here: bf16, 16 sequences of up to 8 new tokens
+// 24.8 us by that one, 30.1 here; of 12: 25.0 and 33.7; int8: 28.7 and 36.0; but
+// a single sequence of 5: 15.6 and 14.8, int8 16.5 and 13.6); with fewer it is
+// slower (attn_rows.cuh has one row each).
 template <int D, bool I8, int NR>
 bl_status attn_rows_launch(PagedAttnArgs& a, int dev, const DeviceInfo& info, unsigned long long* counters,
                            cudaStream_t stream) {

@@ -47,6 +47,7 @@ BAD = [
     (dict(format=1, k_step=A, v_step=A, stride_head=136), {}, ALIGN),  # 16 bytes are 16 codes
     ({}, dict(batch=-1), SHAPE),
     ({}, dict(batch=2 ** 31), SHAPE),
+    ({}, dict(batch=2 ** 31 - 1), SHAPE),
     ({}, dict(max_pages=-1), SHAPE),
     ({}, dict(max_pages=2 ** 26 + 1), SHAPE),
     ({}, dict(cu_q=None), NULL),

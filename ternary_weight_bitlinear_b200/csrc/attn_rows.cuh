@@ -24,9 +24,11 @@
 //    through shared memory; of the CTAs that hold parts of one item the last
 //    to arrive merges them (in groups where there are many), in the order of
 //    the CTAs, so the result does not depend on which it is.  One launch.
-// Bound by what a warp can do with a chunk at a time: its loads' latency, and
-// with int8 the conversions (ALU pipe 60 % busy).  Measured, one new row a
-// sequence: 64 sequences of 3800 positions on average, 20/5 heads of 128, int8:
+// Bound by some 10 us of latency (launch, plan, first loads, merge) and the
+// stream behind it; with int8 by the conversions too (ALU pipe 60 % busy): with
+// the consumers' arithmetic left out the cases below take 59.5, 31.6 and 9.9 us.
+// Ten consumer warps for int8 (144 registers each): 77.8.  Measured, one new row
+// a sequence: 64 sequences of 3800 positions on average, 20/5 heads of 128, int8:
 // 71 us, 4.55 TB/s of the cache (0.69 of the measured copy rate); two of 107,000
 // with one key/value head, bf16: 33 us, 3.3 TB/s; one of 2048, bf16: 10.4 us, of
 // which the launch, the plan and the merge are most (its bytes take 0.8).

@@ -187,6 +187,20 @@ def test_a_nan_among_the_new_rows(n, L, d, fmt, guard):
     assert (np.abs(got[:-1] - want) <= attention_error_bound(want, absv, mag, seen, d)).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+@pytest.mark.parametrize("n,L,d", [(3, 3, 128), (3, 700, 64), (70, 70, 128), (70, 900, 64)])
+def test_a_nan_query_reaches_its_own_row_only(n, L, d, fmt, guard):
+    """Rows share products: a NaN or an infinity in one head of one token stays there."""
+    p = Paged(guard, [n, 2], [L, 40], 16, 2, d, fmt, seed=L + d)
+    q = bf16_values(np.random.default_rng(n), (n + 2, 8, d))
+    bad = q.copy()
+    bad[1, 3, 7], bad[n - 1, 6, 0] = np.nan, np.inf
+    a, b = (B.bitlinear_attn_paged(bf16_dev(bits(x)), p.cache, p.batch, d ** -0.5) for x in (q, bad))
+    own = torch.zeros(n + 2, 8, dtype=torch.bool, device="cuda")
+    own[1, 3] = own[n - 1, 6] = True
+    assert torch.equal(a[~own], b[~own]) and torch.isnan(b[1, 3]).all() and not torch.isfinite(b[n - 1, 6]).any()
+
+
 def test_rows_that_overlap_are_refused(guard):
     p = Paged(guard, [3], [20], 16, 1, 64, "bf16", seed=85)
     w = torch.zeros((4, 8, 64), dtype=torch.bfloat16, device="cuda")

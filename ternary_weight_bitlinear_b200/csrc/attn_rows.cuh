@@ -19,6 +19,10 @@
 //    registers, in the order in which shared memory gives them up in whole
 //    16-byte words: the positions and dimensions of a product may stand in any
 //    order as long as both operands agree.
+//  * What a row does not see has no part in it: probability zero times an
+//    infinity or NaN would be NaN, so a position that only some of an item's
+//    rows see (among its last 15) and that holds one is left out of the
+//    product, and added row by row to those that see it.
 //  * Items ((sequence, head, 16 rows) times their chunks) are shared out
 //    evenly over the CTAs as in attn_paged.cuh.  The warps of a CTA merge
 //    through shared memory; of the CTAs that hold parts of one item the last
@@ -237,6 +241,19 @@ __device__ __forceinline__ int rw_column(int d) {
     return d;
 }
 
+// Which of positions [from, to) of a chunk (bf16) hold an infinity or NaN among
+// their values, a bit each, for a whole warp.
+template <int D>
+__device__ __forceinline__ uint32_t rw_non_finite(const uint8_t* vtile, int from, int to, int lane) {
+    if (from >= to) return 0;
+    uint32_t bad = 0;
+    for (int e = from * 8 + lane; e < to * 8; e += 32)
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h)
+            if (kv_absmax8(*reinterpret_cast<const uint4*>(vtile + h * kRwChunk * 128 + e * 16)) >= 0x7F80u) bad |= 1u << (e >> 3);
+    return __reduce_or_sync(0xffffffffu, bad);
+}
+
 template <int D, bool I8, int NR>
 __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kernel(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -259,7 +276,6 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
     int64_t* warp_sums = plan + 8;                                      // 16 words
     KvSeq* seq = reinterpret_cast<KvSeq*>(plan + 26);
     volatile int* last_flag = reinterpret_cast<volatile int*>(plan + 24);
-    unsigned* bad_rows = reinterpret_cast<unsigned*>(plan + 25);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -275,7 +291,6 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
         mbar_init(got_bar, W);
         mbar_init(sent_bar, W);
         mbar_init(told_bar, 1);
-        *bad_rows = 0;
         mbar_init_fence();
     }
     if (warp == 0 && lane == 0) {
@@ -583,6 +598,35 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                         }
                         __syncwarp();
                     }
+                    // positions [from, to) are hidden from some of the item's rows
+                    const int from = max(vmin - t * kRwChunk, 0), to = min(valid, kRwChunk);
+                    const uint32_t bad = rw_non_finite<D>(vtile, from, to, lane);
+                    for (uint32_t left = bad; left; left &= left - 1) {
+                        const int y = __ffs(left) - 1;
+#pragma unroll
+                        for (int x = 0; x < X; ++x)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                // its probability for row 8 x + 2 kq + j, as the products take it
+                                const uint32_t w2 = y < 16 ? (y < 8 ? p[0][x][0] : p[0][x][1]) : (y < 24 ? p[1][x][0] : p[1][x][1]);
+                                const uint32_t both = __shfl_sync(0xffffffffu, w2, (2 * kq + j) * 4 + ((y & 7) >> 1));
+                                if (t * kRwChunk + y >= vend[x][j]) continue;
+                                const float e = __uint_as_float((y & 1) ? both & 0xFFFF0000u : both << 16);
+#pragma unroll
+                                for (int db = 0; db < D / 16; ++db)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h) {
+                                        const int ch = 2 * (db & 3) + h;
+                                        const uint16_t v = *reinterpret_cast<const uint16_t*>(
+                                            vtile + (db >> 2) * kRwChunk * 128 + y * 128 + ((ch ^ (y & 7)) << 4) + r8 * 2);
+                                        o[db][x][2 * h + j] = fmaf(e, bf16_bits_to_float(v), o[db][x][2 * h + j]);
+                                    }
+                            }
+                        __syncwarp();
+                        if (lane < D / 8)
+                            *reinterpret_cast<uint4*>(vtile + (lane >> 3) * kRwChunk * 128 + y * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        __syncwarp();
+                    }
                 }
 #pragma unroll
                 for (int pb = 0; pb < 2; ++pb) {
@@ -681,7 +725,6 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                         n_1 = fmaf(f, src[rw_column<D, I8>(d + 1)], n_1);
                     }
                 }
-                if (!I8 && !(n_0 * 0.0f == 0.0f && n_1 * 0.0f == 0.0f)) atomicOr(bad_rows, 1u << r);
                 if (whole) {
                     const int row = item->row0 + r, tok = a.by_group.div(row);
                     const int ve = a.causal ? item->vbase + tok + 1 : item->len;
@@ -694,41 +737,6 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(got_bar);
-            if constexpr (!I8) {
-                // an infinity or NaN came out: where it stands in a position that the row does not see, the row is
-                // computed from what it sees alone (as in attn_paged.cuh)
-                ok = __all_sync(0xffffffffu, mbar_wait(got_bar, merges & 1u));
-                if (!ok) break;
-                const unsigned bad = *reinterpret_cast<volatile unsigned*>(bad_rows);
-                const int last = bad ? pa_last_non_finite<D>(a, item->b, item->g, max(vmin, t0 * kRwChunk), min(end, t1 * kRwChunk)) : -1;
-                for (int r = w; bad && r < rows; r += W) {
-                    if (!((bad >> r) & 1)) continue;
-                    const int row = item->row0 + r, tok = a.by_group.div(row);
-                    const int ve = a.causal ? min(max(item->vbase + tok + 1, 0), item->len) : item->len;
-                    if (last < ve) continue;
-                    const int64_t at = item->q0 + tok, head = head0 + a.by_group.mod(row);
-                    float x[D / 32], m2, l2;
-                    pa_row<D>(a, item->b, item->g, a.q + at * a.q_stride + head * D, t0 * kRwChunk,
-                              min(ve, t1 * kRwChunk), x, &m2, &l2);
-#pragma unroll
-                    for (int e = 0; e < D / 32; ++e) {
-                        const int d = lane * (D / 32) + e;
-                        if (whole)
-                            a.out[at * a.o_stride + head * D + d] = float_to_bf16_bits(ve > 0 ? x[e] / l2 : 0.0f);
-                        else
-                            a.part[(prow + r) * D + d] = x[e];
-                    }
-                    if (!whole && lane == 0) *reinterpret_cast<float2*>(a.part_ml + (prow + r) * 2) = make_float2(m2, l2);
-                }
-                if (bad) {  // cleared before the next item's results are looked at
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sent_bar);
-                    ok = __all_sync(0xffffffffu, mbar_wait(sent_bar, sent & 1u));
-                    if (!ok) break;
-                    ++sent;
-                    if (ct == 0) *bad_rows = 0;
-                }
-            }
             ++merges;
             if (!whole) {
                 // ---- merge the item's parts over the CTAs ----

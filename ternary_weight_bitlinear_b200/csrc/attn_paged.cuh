@@ -35,6 +35,15 @@
 //    probabilities (V) in binary32.
 //  * Rows behind an item's last position are no part of the values' product:
 //    its K extent ends at the last 16 positions, where the rows left are zeroed.
+//  * Probability zero times an infinity or NaN in a hidden position is NaN.
+//    Where a row comes out non-finite that such a position may have made so,
+//    the CTA goes over its items a second time: in the steps that only some of
+//    a sub-tile's rows see (its own last tokens) the hidden values are looked
+//    through, and a run of 16 positions with an infinity or NaN among them is
+//    left out of the product and added by the softmax threads, each row over
+//    what it sees.  (Looking in the first pass costs a prompt of 2000
+//    tokens without any 2 %, with as many key/value heads as query heads 5 %.
+//    A prompt of 2048 with a NaN in every page takes 159 us instead of 52.)
 // The running maximum moves only when a tile's exceeds it by 2^8 (the sums
 // stay far inside binary32), so O is seldom rescaled.
 // Bound by the exponentials and the instructions around them, under the power
@@ -135,6 +144,21 @@ __device__ __forceinline__ int pa_end(const PagedAttnArgs& a, const KvSeq& s, in
 __device__ __forceinline__ int pa_items(const PagedAttnArgs& a, int n) {
     const int subs = (n + a.tokens - 1) / a.tokens;
     return (subs + 1) / 2;
+}
+// Positions that the first token of an item's sub-tile sees.
+__device__ __forceinline__ int pa_first(const PagedAttnArgs& a, const PaItem& it, int sub) {
+    return a.causal ? min(max(it.vend + sub * a.tokens, 0), it.len) : it.len;
+}
+// The positions of step u that a sub-tile's product with the values takes while
+// some of its rows do not see them: from the first that its first token does not
+// see to the end of the last run of 16, or the item's last position.
+struct PaSpan {
+    int from, to;  // in the step
+    __device__ __forceinline__ bool some() const { return from < to; }
+};
+__device__ __forceinline__ PaSpan pa_hidden(int first, int own_end, int item_end, int u) {
+    const int at = u * kPaStep;
+    return {max(first - at, 0), min((min(kPaStep, own_end - at) + 15) & ~15, item_end - at)};
 }
 // Cost of item i of a sequence, and its shape.
 __device__ __forceinline__ int pa_cost(const PagedAttnArgs& a, const KvSeq& s, int i, int* nsub, int* nt) {
@@ -445,6 +469,14 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* r) {
         : "r"(taddr));
 }
 
+// One column of this thread's lane.
+__device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+    tmem_ld_wait();
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -501,94 +533,76 @@ __device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
         : "+f"(x), "+f"(y) : "f"(bx), "f"(by));
 }
 
-// ---- one row by a warp ---------------------------------------------------------
-// The (max, sum, vector) of one row over positions [j0, j1) straight from the
-// cache, D/32 dimensions a lane, bf16 pages: only the positions that the row
-// sees take part, whatever the others hold.  32 positions at a time: a lane
-// scores one, then the warp adds the values position by position.  (Seldom
-// needed: 9 us for each 32 positions of a row where every warp of the GPU is
-// at it.)
-template <int D>
-__device__ __noinline__ void pa_row(const PagedAttnArgs& a, int b, int g, const uint16_t* qrow, int j0, int j1,
-                                    float (&o)[D / 32], float* m_out, float* l_out) {
-    constexpr int DL = D / 32;
-    const int lane = threadIdx.x & 31;
-    float m = -INFINITY, l = 0.0f;
+// ---- infinities and NaN among hidden values --------------------------------------
+// Whether rows [from, to) of a bf16 tile of values hold an infinity or NaN,
+// for a whole warp (rows 128 bytes long, their halves HALF bytes apart): such a
+// value times zero is NaN, any other is zero.
+template <int D, int HALF>
+__device__ __forceinline__ bool pa_non_finite(const uint8_t* tile, int from, int to, int lane) {
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.0f, 0.0f);
+    __nv_bfloat162 acc[2] = {zero, zero};
+    for (int e = from * 8 + lane; e < to * 8; e += 32)
 #pragma unroll
-    for (int e = 0; e < DL; ++e) o[e] = 0.0f;
-    for (int j = j0; j < j1; j += 32) {
-        const int p = j + lane;
-        const int page = p < j1 ? kv_page(a.c, a.b, b, p) : -1;
-        const int64_t off = max(page, 0) * a.c.sp + a.c.by_page.mod(p) * a.c.ss + g * a.c.sh;
-        const uint4* k8 = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.k) + off);
-        float x = 0.0f;
+        for (int h = 0; h < D / 64; ++h) {
+            const uint4 v = *reinterpret_cast<const uint4*>(tile + h * HALF + e * 16);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-            const uint4 qv = __ldg(reinterpret_cast<const uint4*>(qrow) + e), kv = __ldcg(k8 + e);
-            const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, kw[4] = {kv.x, kv.y, kv.z, kv.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                x = fmaf(__uint_as_float(qw[y] << 16), __uint_as_float(kw[y] << 16), x);
-                x = fmaf(__uint_as_float(qw[y] & 0xFFFF0000u), __uint_as_float(kw[y] & 0xFFFF0000u), x);
-            }
+            for (int i = 0; i < 4; ++i) acc[i & 1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), zero, acc[i & 1]);
         }
-        x = page >= 0 ? x * a.qscale : -INFINITY;
-        const float mn = fmaxf(m, warp_max_f(x));
-        const float alpha = m == mn ? 1.0f : exp2f(m - mn);
-        const float w = page < 0 || (mn == -INFINITY && x == x) ? 0.0f : exp2f(x - mn);
-        l = fmaf(l, alpha, warp_sum_f(w));
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < DL; ++e) o[e] *= alpha;
-        const uint32_t some = __ballot_sync(0xffffffffu, page >= 0);
-#pragma unroll 16
-        for (int i = 0; i < 32; ++i) {
-            // (a lane without a page stands at page 0, which every cache has)
-            const uint16_t* v = static_cast<const uint16_t*>(a.c.v) + __shfl_sync(0xffffffffu, off, i) + lane * DL;
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            uint32_t vw[DL / 2];
-            if constexpr (DL == 4) {
-                const uint2 y = __ldcg(reinterpret_cast<const uint2*>(v));
-                vw[0] = y.x;
-                vw[1] = y.y;
-            } else {
-                vw[0] = __ldcg(reinterpret_cast<const uint32_t*>(v));
-            }
-            if (!((some >> i) & 1u)) continue;
-#pragma unroll
-            for (int e = 0; e < DL; ++e)
-                o[e] = fmaf(wi, __uint_as_float((e & 1) ? vw[e / 2] & 0xFFFF0000u : vw[e / 2] << 16), o[e]);
-        }
-        bool done = true;  // a NaN stays one: nothing changes any more
-#pragma unroll
-        for (int e = 0; e < DL; ++e) done = done && o[e] != o[e];
-        if (__all_sync(0xffffffffu, done)) break;
-    }
-    *m_out = m;
-    *l_out = l;
+    const __nv_bfloat162 sum = __hadd2(acc[0], acc[1]);
+    return __any_sync(0xffffffffu, (*reinterpret_cast<const uint32_t*>(&sum) & 0x7FFF7FFFu) != 0);
 }
 
-// The last position of [j0, j1) whose value row (bf16 pages) holds an infinity
-// or NaN, for a whole warp; -1 when none does.
-template <int D>
-__device__ __noinline__ int pa_last_non_finite(const PagedAttnArgs& a, int b, int g, int j0, int j1) {
-    constexpr int LANES = D / 8, PER = 32 / LANES;  // lanes of a row, rows at once
-    const int lane = threadIdx.x & 31;
-    for (int j = j1; j > j0; j -= 4 * PER) {
-        int last = -1;
+// Which of the runs of 16 positions of a step hold one in rows [from, to), a bit each.
+template <int D, int HALF>
+__device__ __noinline__ uint32_t pa_runs_non_finite(const uint8_t* tile, int from, int to, int lane) {
+    uint32_t runs = 0;
+    for (int e = from * 8 + lane; e < to * 8; e += 32)
 #pragma unroll
-        for (int u = 3; u >= 0; --u) {
-            const int p = j - 1 - u * PER - lane / LANES;
-            const int page = p >= j0 ? kv_page(a.c, a.b, b, p) : -1;
-            if (page < 0) continue;
-            const int64_t off = page * a.c.sp + a.c.by_page.mod(p) * a.c.ss + g * a.c.sh;
-            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.c.v) + off) + lane % LANES);
-            if (kv_absmax8(v) >= 0x7F80u) last = p;
+        for (int h = 0; h < D / 64; ++h)
+            if (kv_absmax8(*reinterpret_cast<const uint4*>(tile + h * HALF + e * 16)) >= 0x7F80u) runs |= 1u << (e >> 7);
+    return __reduce_or_sync(0xffffffffu, runs);
+}
+
+// The products of a step's probabilities p (bf16 pairs, tensor memory) and
+// values over those runs, added to this thread's row of the output o (in tensor
+// memory too; begun at zero when `fresh`): over the `vis` positions of the step
+// that the row sees and no others.  (Seldom needed: some 25 us a run.)
+template <int D, int HALF>
+__device__ __noinline__ void pa_add_runs(uint32_t o, uint32_t p, const uint8_t* tile, uint32_t runs, int vis, bool fresh) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t r[32];
+        if (fresh) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0;
+        } else {
+            tmem_ld32(o + c, r);
         }
-        last = __reduce_max_sync(0xffffffffu, last);
-        if (last >= 0) return last;
+#pragma unroll 1
+        for (int j = 0; j < kPaStep; ++j) {
+            if (!((runs >> (j >> 4)) & 1u)) continue;
+            __syncwarp();
+            const uint32_t pair = tmem_ld1(p + (j >> 1));
+            if (j >= vis) continue;
+            const float x = __uint_as_float((j & 1) ? pair & 0xFFFF0000u : pair << 16);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint4 v = *reinterpret_cast<const uint4*>(tile + (c >> 6) * HALF + sw128_offset(j, ((c & 63) >> 3) + y));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t& lo = r[8 * y + 2 * i];
+                    uint32_t& hi = r[8 * y + 2 * i + 1];
+                    lo = __float_as_uint(fmaf(x, __uint_as_float(w[i] << 16), __uint_as_float(lo)));
+                    hi = __float_as_uint(fmaf(x, __uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(hi)));
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st32(o + c, r);
     }
-    return -1;
+    tmem_st_wait();
 }
 
 // ---- the kernel -----------------------------------------------------------------
@@ -628,6 +642,9 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     int64_t* warp_sums = plan + 8;                                      // 16 words
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan + 24);
     KvSeq* seq = reinterpret_cast<KvSeq*>(plan + 26);
+    // runs of 16 positions that a product with the values leaves out: of group w's step in buffer j & 1
+    volatile uint32_t* left_out = reinterpret_cast<volatile uint32_t*>(plan + 28);
+    unsigned* redo = reinterpret_cast<unsigned*>(plan + 30);            // bit 0: the share is gone over again, bit 1: a wait ran out
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -659,6 +676,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             mbar_init(ifull_bar(i), 1);
             mbar_init(iempty_bar(i), I8 ? 15 : 11);  // page loader, MMA issuers, softmax (and converter) warps
         }
+        *redo = 0;
         mbar_init_fence();
     }
     if (warp == 1) tmem_alloc(smem_addr(tmem_slot), 512);
@@ -685,14 +703,31 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         if (lane == 0) mbar_arrive(iempty_bar(ii));
         ++ii;
     };
+    // Every role goes over the CTA's items once, and where a row came out non-finite that an infinity or NaN in a hidden
+    // position may have made so, once more with a look at those positions (see PaSpan).  Every warp asks once, with
+    // nothing of its own under way in tensor memory, so that the CTA may end without another barrier.
+    bool careful = false;
+    auto again = [&](bool takes) {
+        if constexpr (!I8) {  // (codes are finite)
+            if (careful) return false;
+            if (!ok) atomicOr(redo, 2u);
+            tc_fence_before();
+            __syncthreads();
+            careful = *reinterpret_cast<volatile unsigned*>(redo) == 1u;
+            if (careful && takes) release();  // the items' end
+        }
+        return careful;
+    };
     if (warp < 4) {
     setmaxnreg_dec<C::kRegsRest>();
     if (warp == 3) {
         // ---------------- scheduler, and the queries: one slot per sub-tile ----------------
+        uint32_t n = 0, flying = 0;
+        do {
         if (lane == 0) {
             PaWalk walk(a, plan, seq);
+            walk.slot = (int)n;
             PaItem it;
-            uint32_t n = 0, flying = 0;
             for (bool more = true; more && ok; ++ii) {
                 more = walk.next(it);
                 if (!more) {
@@ -718,6 +753,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             if (!ok)
                 for (uint32_t j = flying; j < n; ++j) mbar_wait(qfull_bar((int)(j & 1)), (j >> 1) & 1u);
         }
+        } while (again(false));
     } else if (warp == 0) {
         // ---------------- pages: K and V tiles (and steps) ----------------
         constexpr int NR = I8 ? C::kRaw : NS;
@@ -725,6 +761,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         uint32_t n = 0;        // ring places used (K and V in turn)
         uint32_t flying = 0;   // oldest place that may still be landing
         uint32_t tile = 0, tile_flying = 0;
+        do {
         while (const PaItem* item = take()) {
             const PaItem it = *item;
             release();
@@ -779,6 +816,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             }
             if (!ok) break;
         }
+        } while (again(true));
         // after a failed wait, let the copies still in flight land first
         if (!ok && lane == 0) {
             for (uint32_t j = flying; j < n; ++j)
@@ -813,29 +851,32 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         };
         auto finish = [&]() {  // O (+)= P V of step `used`
             const uint32_t x = used & 1 ? info1 : info0;
-            const int st = (int)(x & 0xFF), half = (int)(x >> 8) & 1, ksteps = (int)(x >> 12);
+            const int st = (int)(x & 0xFF), half = (int)(x >> 8) & 1, ksteps = (int)(x >> 12) & 7;
             if (!wait(full_bar(st), (x >> 9) & 1u) || !wait(prob_bar(w, used), (used >> 1) & 1u)) return;
             tc_fence_after();
             const uint64_t vd = pa_desc_v(base + C::kOffRing + st * C::kTileBytes + half * (kPaStep * 128), C::kHalfBytes);
-            const uint32_t p = sc + 64u * (used & 1), add = (x >> 10) & 1u ? 0u : 1u;
+            const uint32_t out = !I8 && (x >> 15) ? (uint32_t)uniform((int)left_out[2 * w + (used & 1)]) : 0u;
+            const uint32_t p = sc + 64u * (used & 1), add = (x >> 10) & 1u && !out ? 0u : 1u;  // (the group began O where it left some out)
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kPaStep / 16; ++k)  // 16 positions: 8 columns of P, two 8-row groups of V
-                    if (k < ksteps) tc_mma_f16_ts(oc, p + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), k ? 1u : add);
+                    if (k < ksteps && !((out >> k) & 1u)) tc_mma_f16_ts(oc, p + 8u * k, vd + (uint64_t)(k * 2048 >> 4), pa_idesc_pv<D>(), k ? 1u : add);
                 tc_commit(pv_bar(w, used));
                 if ((x >> 11) & 1u) tc_commit(empty_bar(st));
             }
             __syncwarp();
             ++used;
         };
+        do {
         while (ok) {
             if (!wait(ifull_bar(ii), (ii / kPaItems) & 1u)) break;
             const PaItem& it = ring[ii % kPaItems];
             if (uniform(it.b) < 0) break;
             const bool pair = uniform(it.nsub) == 2;
             const int t0 = uniform(it.t0), t1 = uniform(it.t1), nq = uniform(it.nq);
-            const int end = uniform(pair && w == 0 ? it.end0 : it.end);
+            const int item_end = uniform(it.end), end = pair && w == 0 ? uniform(it.end0) : item_end;
             const uint32_t slot = (uint32_t)uniform(it.slot);
+            const int first = I8 ? 0 : uniform(pa_first(a, it, pair ? w : 0));
             release();
             // this group's Q tile (a single item's one is both groups')
             const uint32_t own = slot + (nq == 2 ? w : 0);
@@ -878,9 +919,11 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                     }
                     __syncwarp();
                     const int valid = min(kPaStep, end - (2 * t + h) * kPaStep);
-                    // ring place, half, its phase, first step of the item, last of the tile, products of 16 positions
+                    // ring place, half, its phase, first step of the item, last of the tile, products of 16 positions,
+                    // whether runs of 16 may be left out
                     const uint32_t x = (uint32_t)vst | (uint32_t)h << 8 | vph << 9 | (2 * t + h == from ? 1u << 10 : 0u) |
-                                       (h == h1 - 1 ? 1u << 11 : 0u) | (uint32_t)((valid + 15) / 16) << 12;
+                                       (h == h1 - 1 ? 1u << 11 : 0u) | (uint32_t)((valid + 15) / 16) << 12 |
+                                       (!I8 && careful && pa_hidden(first, end, item_end, 2 * t + h).some() ? 1u << 15 : 0u);
                     if (made & 1) info1 = x; else info0 = x;
                     ++made;
                 }
@@ -892,9 +935,10 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         // every MMA this warp issued has finished before TMEM is freed (elect.sync names the same lane every time)
         if (elect_one()) {
             tc_commit(drain_bar(w));
-            mbar_wait(drain_bar(w), 0);
+            mbar_wait(drain_bar(w), careful ? 1u : 0u);
         }
         __syncwarp();
+        } while (again(true));
     }
     } else if (warp >= 12) {
         // ---------------- int8 codes -> bf16 operand tiles ----------------
@@ -956,6 +1000,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
         uint32_t step = 0, merges = 0, tile = 0;  // steps of this group, merges, tiles
         int state = 0;      // of this CTA's first share (see desc)
         int4 began = make_int4(0, 0, 0, 0);
+        do {
         while (const PaItem* item = take()) {
             const bool pair = item->nsub == 2;
             const int t0 = item->t0, t1 = item->t1, end = item->end;
@@ -965,7 +1010,9 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             const bool warp_live = quad * 32 < tokens * a.group;
             // positions that this row sees (a lane without a row is masked nowhere: its results go nowhere)
             const int vend = !live ? kNoMask : a.causal ? min(max(item->vend + sub * a.tokens + tok, 0), item->len) : item->len;
-            const int to = min(2 * t1, ((pair && w == 0 ? item->end0 : end) + kPaStep - 1) / kPaStep);
+            const int own = pair && w == 0 ? item->end0 : end;
+            const int first = pa_first(a, *item, sub);
+            const int to = min(2 * t1, (own + kPaStep - 1) / kPaStep);
             const uint32_t step0 = step;
             float m = -INFINITY, l = 0.0f;
             for (int t = t0; t < t1; ++t, ++tile) {
@@ -1072,18 +1119,39 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                         l += (l0 + l1) + (l2 + l3);
                         tmem_st_wait();
                     }
-                    if (!I8 && valid < kPaStep && valid % 16 != 0) {
-                        // values behind the last position that anything sees, in the last 16 that the product reads: zeros
-                        // (probability zero times whatever the page holds there would not be)
-                        const uint32_t n = 2 * tile + 1;
-                        const int st = (int)(n % NS);
-                        ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (n / NS) & 1u));
-                        if (!ok) break;
-                        const int rows = 16 - valid % 16;
-                        uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes + (h * kPaStep + valid) * 128;
-                        for (int e = quad * 32 + lane; e < rows * 8 * C::kHalves; e += 128)
-                            *reinterpret_cast<uint4*>(vt + e / (rows * 8) * C::kHalfBytes + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
-                        fence_proxy_async_smem();
+                    if constexpr (!I8) {
+                        // The product takes whole runs of 16 positions.  Probability zero times an infinity or NaN would
+                        // not be zero, so values behind the last position that anything sees are zeroed, and runs with
+                        // such values where some row does not see them are left to this group's threads.
+                        const bool tail = valid < kPaStep && valid % 16 != 0;
+                        PaSpan hidden = {0, 0};
+                        if (careful) hidden = pa_hidden(first, own, end, u);
+                        if (tail || hidden.some()) {
+                            const uint32_t n = 2 * tile + 1;
+                            const int st = (int)(n % NS);
+                            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(st), (n / NS) & 1u));
+                            if (!ok) break;
+                            uint8_t* vt = sm + C::kOffRing + st * C::kTileBytes + h * kPaStep * 128;
+                            if (tail) {
+                                const int rows = 16 - valid % 16;
+                                for (int e = quad * 32 + lane; e < rows * 8 * C::kHalves; e += 128)
+                                    *reinterpret_cast<uint4*>(vt + valid * 128 + e / (rows * 8) * C::kHalfBytes + e % (rows * 8) * 16) = make_uint4(0, 0, 0, 0);
+                                fence_proxy_async_smem();
+                            }
+                            if (hidden.some() && warp_live) {
+                                uint32_t runs = 0;
+                                if (pa_non_finite<D, C::kHalfBytes>(vt, hidden.from, hidden.to, lane)) {
+                                    if (step != step0) {  // the output so far, once the last step's product is in it
+                                        ok = __all_sync(0xffffffffu, mbar_wait(pv_bar(w, step - 1), ((step - 1) >> 1) & 1u));
+                                        if (!ok) break;
+                                        tc_fence_after();
+                                    }
+                                    runs = pa_runs_non_finite<D, C::kHalfBytes>(vt, hidden.from, hidden.to, lane);
+                                    pa_add_runs<D, C::kHalfBytes>(to_o, tb, vt, runs, min(vend, end) - u * kPaStep, step == step0);
+                                }
+                                if (quad == 0 && lane == 0) left_out[2 * w + (step & 1)] = runs;  // (quad 0 has the first row)
+                            }
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -1194,40 +1262,9 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                 __syncwarp();
                 if (live && !whole)
                     *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m == -INFINITY ? m : m * a.qscale, l);
-                if constexpr (!I8) {
-                    // an infinity or NaN came out.  Where it stands in a position that the row does not see (its
-                    // probability there is zero, the product is not), the row is computed from what it sees alone
-                    uint32_t bad = __ballot_sync(0xffffffffu, live && !(poison == 0.0f));
-                    if (bad) {
-                        const int own = pair && w == 0 ? item->end0 : end;  // the product's last 16 may go beyond
-                        const int last = pa_last_non_finite<D>(
-                            a, item->b, item->g, max(__reduce_min_sync(0xffffffffu, vend), t0 * kPaTile),
-                            min(min(end, own + 15), t1 * kPaTile));
-                        bad &= __ballot_sync(0xffffffffu, vend <= last);
-                    }
-                    __syncwarp();
-                    while (bad) {
-                        const int src = __ffs(bad) - 1;
-                        bad &= bad - 1;
-                        const int r2 = quad * 32 + src, tok2 = r2 / a.group, hh2 = r2 % a.group;
-                        const int vend2 = __shfl_sync(0xffffffffu, vend, src);
-                        const int64_t token = item->row + sub * a.tokens + tok2;
-                        const int64_t head = item->g * a.group + hh2;
-                        float o[D / 32], m2, l2;
-                        pa_row<D>(a, item->b, item->g, a.q + token * a.q_stride + head * D, t0 * kPaTile,
-                                  min(vend2, t1 * kPaTile), o, &m2, &l2);
-                        const int64_t prow2 = ((int64_t)blockIdx.x * 2 + slot) * a.part_rows + sub * kPaRows + r2;
-#pragma unroll
-                        for (int e = 0; e < D / 32; ++e) {
-                            if (whole)
-                                a.out[token * a.o_stride + head * D + lane * (D / 32) + e] =
-                                    float_to_bf16_bits(vend2 > 0 ? o[e] / l2 : 0.0f);
-                            else
-                                a.part[prow2 * D + lane * (D / 32) + e] = o[e];
-                        }
-                        if (!whole && lane == 0) *reinterpret_cast<float2*>(a.part_ml + prow2 * 2) = make_float2(m2, l2);
-                    }
-                }
+                // an infinity or NaN came out of products that took positions which the row does not see
+                if (!I8 && !careful && live && !(poison == 0.0f) && vend < min(min(end, (own + 15) & ~15), t1 * kPaTile)) atomicOr(redo, 1u);
+                __syncwarp();
             }
             if (merge) {
                 tc_fence_before();
@@ -1248,14 +1285,17 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
             if (!ok) break;
             release();
         }
+        } while (again(true));
         if (w == 0 && quad == 0 && lane == 0) {
             a.desc[2 * blockIdx.x] = make_int4(state, 0, 0, 0);
             a.desc[2 * blockIdx.x + 1] = began;
         }
     }
 
-    tc_fence_before();
-    __syncthreads();
+    if (I8 || careful) {
+        tc_fence_before();
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);

@@ -24,7 +24,7 @@ def spoil(p, share, seed):
     one always."""
     rng = np.random.default_rng(seed)
     for b, (n, L) in enumerate(zip(p.new, p.lens)):
-        for pos in range(L - n, L):
+        for pos in range(max(L - n, 0), L):
             if pos == L - 1 or rng.random() < share:
                 at = p.pages[b][pos // p.page], pos % p.page
                 dims = rng.integers(0, p.d, 3)
@@ -35,10 +35,13 @@ def spoil(p, share, seed):
 # new rows, positions, heads of a group, head size; up to 16 rows of a head a sequence
 FEW = [([4], [40], 4, 64), ([16], [300], 1, 128), ([5], [37], 3, 64), ([2, 2], [33, 1500], 8, 128), ([8], [8], 2, 64),
        ([4, 0, 3], [5000, 3, 64], 4, 128), ([2], [2], 7, 128), ([2], [100], 4, 128), ([8], [20], 1, 64)]
+# more
+MANY = [([64], [64], 4, 64), ([200], [333], 1, 128), ([70], [900], 12, 64), ([33], [33], 7, 128), ([300, 5], [300, 2000], 4, 128),
+        ([20, 0, 90], [3, 9, 1500], 2, 64), ([130], [130], 1, 64), ([1, 70], [5000, 3000], 16, 128), ([2], [700], 100, 64)]
 
 
 @pytest.mark.parametrize("share", [0.1, 1.0])
-@pytest.mark.parametrize("new,lens,group,d", FEW)
+@pytest.mark.parametrize("new,lens,group,d", FEW + MANY)
 def test_non_finite_values_among_the_new_rows(new, lens, group, d, share, guard):
     p = Paged(guard, new, lens, 16, 2, d, "bf16", seed=sum(lens) + d)
     spoil(p, share, seed=group)
@@ -60,7 +63,7 @@ def test_non_finite_values_among_the_new_rows(new, lens, group, d, share, guard)
     assert (np.abs(got - np.where(ok, want, 0))[ok] <= bound[ok]).all()
 
 
-LONG = [(2, 8, 2 ** 21, 128)]
+LONG = [(2, 8, 2 ** 21, 128), (16, 8, 2 ** 18, 64), (16, 8, 2 ** 18, 128)]
 
 
 @pytest.mark.parametrize("n,group,L,d", LONG)

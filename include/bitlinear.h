@@ -525,7 +525,8 @@ bl_status bitlinear_kv_write(const bl_kv_cache* cache, const bl_kv_batch* batch,
  * the cache, RN_bf16(RN32(code * step)) for BL_KV_I8 (with cu_q counting every
  * position of a sequence, the whole of it).  Rows that belong to no sequence,
  * or whose position is negative, are left as they were.  k, v, strides and T
- * as for bitlinear_kv_write, as outputs. */
+ * as for bitlinear_kv_write, as outputs, which must not overlap (BL_ERR_SHAPE);
+ * both may be slices of the rows of one tensor. */
 bl_status bitlinear_kv_read(const bl_kv_cache* cache, const bl_kv_batch* batch, uint16_t* k,
                             int64_t k_stride, uint16_t* v, int64_t v_stride, int64_t T, void* stream);
 

@@ -505,8 +505,8 @@ def bitlinear_kv_write(k, v, cache, batch, stream=None):
 
 def bitlinear_kv_read(cache, batch, T=None, k=None, v=None, stream=None):
     """The rows of a batch read back out of the cache: (k, v) bf16 [T, kv_heads,
-    head_dim], into the given tensors or new ones of T rows.  Rows of no sequence
-    are left as they were (in a new tensor: zeros)."""
+    head_dim], into the given tensors (which must not overlap) or new ones of T
+    rows.  Rows of no sequence are left as they were (in a new tensor: zeros)."""
     heads, d, dev = _kv_facts(cache, batch)
     if k is None or v is None:
         if T is None:

@@ -1481,6 +1481,7 @@ bl_status bitlinear_kv_read(const bl_kv_cache* cache, const bl_kv_batch* batch, 
     int dev;
     DeviceInfo info;
     if ((st = current_device(&dev, &info)) != BL_OK) return st;
+    if (rows_overlap(k, k_stride, v, v_stride, T, width)) return BL_ERR_SHAPE;
     const bool i8 = cache->format == BL_KV_I8;
     const bool many = kv_many(cache, T, info.sms);
     auto kernel = cache->head_dim == 128

@@ -227,3 +227,21 @@ def test_cache_past_two_gi_elements(guard):
     assert int((kp != 0).sum()) == int((code != 0).sum())
     k, _ = B.bitlinear_kv_read(cache, batch, T=3)
     assert same(f32_of_bf16(bf16_host(k)), torch.from_numpy(OK.dequantise(code, step)).to(torch.bfloat16).float().numpy())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_rows_read_into_each_other_are_refused(fmt, guard):
+    """k and v into one tensor: refused where they share elements, right where they take turns within its rows."""
+    p = Paged(guard, [3, 2], [20, 2], 16, 2, 64, fmt, seed=18)
+    w = guard.empty((7, 6, 64), torch.bfloat16, fill=0)
+    one = w[:5, :2]
+    for k, v in ((one, one), (w[:5, :2], w[:5, 1:3]), (w[:5, 2:4], w[1:6, 2:4]), (w[1:6, 1:3], w[:5, 2:4]),
+                 (w[:5, 4:], w[1:6, 3:5])):
+        with pytest.raises(B.BitLinearError) as e:
+            B.bitlinear_kv_read(p.cache, p.batch, k=k, v=v)
+        assert e.value.status == 2
+    assert not w.any()
+    want = [x.clone() for x in B.bitlinear_kv_read(p.cache, p.batch, T=p.T)]
+    for k, v in ((w[:5, :2], w[:5, 2:4]), (w[:5, 4:], w[1:6, :2]), (w[2:, 2:4], w[:5, 4:])):
+        B.bitlinear_kv_read(p.cache, p.batch, k=k, v=v)
+        assert torch.equal(k, want[0]) and torch.equal(v, want[1])

@@ -467,7 +467,8 @@ typedef enum { BL_KV_BF16 = 0, BL_KV_I8 = 1 } bl_kv_format;
  * int8 rows (one position of one key/value head) carry a binary32 step each:
  * a code stands for RN32(code * step).
  *   head_dim 64 or 128; page_size a multiple of 16; k, v 16-byte aligned and
- *   every stride a positive multiple of 16 bytes. */
+ *   every stride a positive multiple of 16 bytes.  The rows of k and v that a
+ *   call writes must not share memory. */
 typedef struct {
     void* k;               /* bf16 or int8 per format */
     void* v;
@@ -543,9 +544,13 @@ bl_status bitlinear_attn_paged_workspace_size(int64_t T, int64_t q_heads, int64_
  * g = h / (q_heads / kv_heads), over the positions j of r's sequence: every
  * one (causal 0), or those up to r's own position kv_len - n + i (causal 1).
  * What a hidden position holds has no part in a result, infinities and NaN
- * included.  A row that sees no position gets zeros.
- * Scores, softmax and sums are binary32; the probabilities are rounded to bf16
- * for the product with the values (relative 2^-8 each), the output to bf16.
+ * included (with such values a prompt takes several times as long).
+ * A row that sees no position gets zeros.
+ * Scores, softmax and sums are binary32, the sum of the weighted values too,
+ * which is divided at the end (weights reach 2^8, so it overflows for values
+ * near the type's largest); the probabilities, times their position's step with
+ * BL_KV_I8, are rounded to bf16 for the product with the values (relative 2^-8
+ * each), the output to bf16.
  *   q, out     device bf16 [T, q_heads, head_dim]; rows q_stride / out_stride
  *              elements apart, heads contiguous; 16-byte aligned, strides
  *              multiples of 8.  Rows of no sequence are left as they were.

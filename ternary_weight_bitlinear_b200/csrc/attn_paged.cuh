@@ -46,12 +46,14 @@
 //    A prompt of 2048 with a NaN in every page takes 159 us instead of 52.)
 // The running maximum moves only when a tile's exceeds it by 2^8 (the sums
 // stay far inside binary32), so O is seldom rescaled.
-// Bound by the exponentials and the instructions around them, under the power
-// limit (XU pipe 51 % busy, tensor pipe 43 %, issue 41 %).  Measured, 20/5 heads
-// of 128: a prompt of 8192 tokens, bf16, 387 to 399 us, 860 TFLOP/s of what the
-// rows see (0.52 of the measured matrix rate); six chunks of up to 600 over 6800
-// positions on average, int8, 270 us, 648 TFLOP/s.  Five documents of up to 1777, 16/2 heads, not
-// causal: 101 us, 640 TFLOP/s.  Tried without gain: a polynomial for some of the
+// No unit is at its rate (prompt of 8192, bf16: XU pipe 44 to 51 % busy, tensor
+// pipe 43 %, issue 41 %; six chunks, int8: 31, 32 and 51 %): the time is the two
+// groups' dependent chains of tensor-memory loads, exponentials and products,
+// under the power limit.  Measured, 20/5 heads of 128: a prompt of 8192 tokens,
+// bf16, 372 to 391 us, 924 to 879 TFLOP/s of what the rows see (0.56 to 0.53 of
+// the measured matrix rate); six chunks of up to 600 over 6800 positions on
+// average, int8, 272 us, 645 TFLOP/s.  Five documents of up to 1777, 16/2 heads, not
+// causal: 102 us, 637 TFLOP/s.  Tried without gain: a polynomial for some of the
 // exponentials, one score buffer with the probabilities beside it, merging in
 // this kernel (one SM's latency: prompts of a few hundred tokens 26 -> 66 us).
 #pragma once
@@ -94,8 +96,7 @@ struct PagedAttnArgs {
     const uint16_t* q;   // bf16 [T, heads, D], rows q_stride apart
     uint16_t* out;       // bf16 [T, heads, D], rows o_stride apart
     int64_t q_stride, o_stride;
-    int heads;
-    int group;           // heads / kv_heads
+    int group;           // query heads of a key/value head
     FastDiv by_group;
     int tokens;          // tokens of a sub-tile: 128 / group
     int causal;
@@ -286,7 +287,6 @@ __device__ __forceinline__ void pa_share(int64_t total, int64_t* u0, int64_t* u1
 // This CTA's share of all units, and the item that its first unit lies in:
 // plan = {u0, u1, first unit of that item, sequence, head, item, all units},
 // seq = that sequence.  Every thread of the CTA calls it; warp_sums has 16 words.
-constexpr int kPaPlanWords = 7;
 template <class Cut>
 __device__ __forceinline__ void pa_plan(const PagedAttnArgs& a, int64_t* plan, KvSeq* seq, int64_t* warp_sums) {
     int64_t total = 0, mine = 0, upto = 0, per = 0;
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
     auto iempty_bar = [&](uint32_t i) { return item_bars + 8u * (kPaItems + i % kPaItems); };
     static_assert(kB2 + 20 + 2 * kPaItems == C::kBars, "barrier count");
     PaItem* ring = reinterpret_cast<PaItem*>(sm + C::kOffItems);
-    int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // kPaPlanWords
+    int64_t* plan = reinterpret_cast<int64_t*>(sm + C::kOffPlan);       // 7 words
     int64_t* warp_sums = plan + 8;                                      // 16 words
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(plan + 24);
     KvSeq* seq = reinterpret_cast<KvSeq*>(plan + 26);
@@ -1097,6 +1097,9 @@ __global__ void __launch_bounds__(PaCfg<D, I8>::kThreads, 1) attn_paged_kernel(
                                 add2(l2, l3, r[e + 2], r[e + 3]);
                             }
                             if constexpr (I8) {
+                                // (before the rounding to bf16, so that a weight is rounded once: the code beside it is exact.
+                                // A probability of one is not exact then: 0.0023 of the outputs' norm is error, 0.0019 with
+                                // a bf16 cache)
                                 const float* vs = ks + kPaTile + h * kPaStep + 32 * c;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4) {

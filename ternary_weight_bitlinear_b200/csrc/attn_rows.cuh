@@ -1,6 +1,6 @@
 // attn_rows.cuh -- attention over the paged cache for batches with few rows a
-// sequence and key/value head (decode steps, a few drafted tokens): the same
-// operation as attn_paged.cuh's, made for streaming the cache.
+// sequence and key/value head on average (decode steps, a few drafted tokens):
+// the same operation as attn_paged.cuh's, made for streaming the cache.
 //
 // With at most 16 rows against each position the products are far below what
 // the keys and values cost to read, so the kernel is built as a stream: a
@@ -34,7 +34,7 @@
 // Ten consumer warps for int8 (144 registers each): 77.8.  Measured, one new row
 // a sequence: 64 sequences of 3800 positions on average, 20/5 heads of 128, int8:
 // 71 us, 4.55 TB/s of the cache (0.69 of the measured copy rate); two of 107,000
-// with one key/value head, bf16: 33 us, 3.3 TB/s; one of 2048, bf16: 10.4 us, of
+// with one key/value head, bf16: 33 us, 3.3 TB/s; one of 2048, bf16: 10.1 us, of
 // which the launch, the plan and the merge are most (its bytes take 0.8).
 // The tensor-memory kernel took 292, 69 and 18.8 us for these.
 #pragma once
@@ -581,7 +581,8 @@ __global__ void __launch_bounds__(RwCfg<D, I8, NR>::kThreads, 1) attn_rows_kerne
                             for (int j = 0; j < 2; ++j) {
                                 e[j] = ex2(s[pb][x][2 * h + j] - ref[j]);
                                 l[x][j] += e[j];
-                                // (a step behind the last position may be anything)
+                                // (a step behind the last position may be anything; rounded to bf16 with the probability,
+                                // as in attn_paged.cuh)
                                 if constexpr (I8) e[j] = masked && p0 + 16 * pb + 8 * h >= vend[x][j] ? 0.0f : e[j] * vs[pb][h];
                             }
                             p[pb][x][h] = movm_t(pack_bf16x2(e[0], e[1]));

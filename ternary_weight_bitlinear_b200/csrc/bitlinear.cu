@@ -940,7 +940,13 @@ int64_t kv_run(const KvCacheArgs& c, int64_t d, int64_t elem_bytes) {
 
 // Few rows against each position (attn_rows.cuh): up to NR a sequence and
 // key/value head on average, 8 (a product's columns) or 16.  The lengths
-// themselves are on the device: either kernel is right for every batch.  With
+// themselves are on the device: either kernel is right for every batch, but the
+// average says little about a batch of unequal ones, whose sequences all go
+// through one kernel.  Slots without rows count too.  20/5 heads of 128, bf16
+// (int8): 64 decode rows and a chunk of 512, through the tensor-memory kernel,
+// 66 us (94), the two alone 49 and 27 (39 and 30); 200 decode rows and the chunk,
+// through this one, 213 (226), alone 124 and 27 (97 and 30); a prompt of 3000 in a
+// batch padded to 1024 slots, through this one, 766 (815), alone 81 (97).  With
 // more rows the tensor-memory kernel is mostly faster (20/5 heads of 128 over
 // 2000 positions, 16 rows an item here: bf16, 16 sequences of up to 8 new tokens
 // 24.8 us by that one, 30.1 here; of 12: 25.0 and 33.7; int8: 28.7 and 36.0; but
@@ -1529,7 +1535,6 @@ bl_status bitlinear_attn_paged(const bl_kv_cache* cache, const bl_kv_batch* batc
     a.out = out;
     a.q_stride = q_stride;
     a.o_stride = out_stride;
-    a.heads = (int)q_heads;
     a.group = (int)(q_heads / cache->kv_heads);
     a.by_group = fast_div(a.group);
     a.causal = causal != 0;

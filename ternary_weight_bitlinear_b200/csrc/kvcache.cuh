@@ -14,14 +14,15 @@
 // an infinity or NaN has no scale: it is written as zero codes with a NaN
 // step, so every reader of that row (and no other) gets NaN.
 //
-// Both kernels move each row once and are bound by HBM bytes (for a few rows
-// by latency).  A group of d/8 lanes (int8: d/16) takes one or several (row,
+// Both kernels move each row once.  bf16 rows are bound by HBM bytes, int8 rows
+// and a few rows by the latency of look-ups and loads (int8: DRAM 23 to 35 %,
+// issue slots under half).  A group of d/8 lanes (int8: d/16) takes one or several (row,
 // head) pairs, 16 bytes of the cache a lane; a warp looks up 32 sequences at
 // once, a lane each, so a row costs two rounds of dependent loads (its
 // sequence, its page) before its own; the row's maximum costs log2(d/16)
-// shuffles.  Measured: 30,000 rows of 8 heads of 64 into a bf16 cache 23.7 us
-// (5.2 TB/s of rows read and written); 43,500 positions of 5 heads of 128 read
-// back from int8 37.9 us (4.45 TB/s); 333 rows read 2.3 us.
+// shuffles.  Measured: 30,000 rows of 8 heads of 64 into a bf16 cache 24.0 us
+// (5.1 TB/s of rows read and written); 43,500 positions of 5 heads of 128 read
+// back from int8 38.2 us (4.4 TB/s); 333 rows read 2.3 us.
 #pragma once
 
 #include <type_traits>
